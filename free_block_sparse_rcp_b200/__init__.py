@@ -77,7 +77,71 @@ class ProbeTrace(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("probe_o_sparse", "probe_lse_dense", "probe_lse_sparse", "sigma", "b_sub")]
 
 
+BF16, FP16, FP32 = 0, 1, 2
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def _dtype_code(dt) -> int:
+    """SPARSEPR_BF16 / FP16 / FP32 of a torch dtype (integers pass through)."""
+    if isinstance(dt, int):
+        return dt
+    import torch
+    codes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+    if dt not in codes:
+        raise ValueError(f"unsupported dtype {dt}")
+    return codes[dt]
+
+
+_ll3 = ctypes.c_longlong * 3
+_ll2 = ctypes.c_longlong * 2
+
+
+class RopeParams(ctypes.Structure):
+    """Mirror of ``sparsepr_rope_params``."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "H", "N", "d", "H2", "dtype", "rot_dim", "layout", "n_axes")] + \
+               [("axis_dim", ctypes.c_int * 3)] + \
+               [(n, ctypes.c_int) for n in ("pos_batched", "scaling", "orig_len")] + \
+               [(n, ctypes.c_double) for n in ("theta", "factor", "beta_fast", "beta_slow", "magnitude")] + \
+               [(n, _ll3) for n in ("x_stride", "y_stride", "x2_stride", "y2_stride")]
+
+    @classmethod
+    def make(cls, B, H, N, d, *, H2=0, dtype=BF16, rot_dim=None, layout="half", axis_dim=None, pos_batched=0,
+             scaling="none", orig_len=0, theta=10000.0, factor=1.0, beta_fast=32.0, beta_slow=1.0, magnitude=0.0):
+        """layout: "half" or "interleaved"; axis_dim: rotated elements per position axis
+        (default one axis of rot_dim); scaling: "none", "linear", "base" or "parts"."""
+        rot = d if rot_dim is None else rot_dim
+        axes = [rot] if axis_dim is None else list(axis_dim)
+        if not 1 <= len(axes) <= 3:
+            raise ValueError("axis_dim must name 1 to 3 axes")
+        p = cls(B=B, H=H, N=N, d=d, H2=H2, dtype=_dtype_code(dtype), rot_dim=rot,
+                layout=ROPE_LAYOUTS.get(layout, layout), n_axes=len(axes), pos_batched=pos_batched,
+                scaling=ROPE_SCALINGS.get(scaling, scaling), orig_len=orig_len, theta=theta, factor=factor,
+                beta_fast=beta_fast, beta_slow=beta_slow, magnitude=magnitude)
+        for i, a in enumerate(axes):
+            p.axis_dim[i] = a
+        return p
+
+
+class CacheParams(ctypes.Structure):
+    """Mirror of ``sparsepr_cache_params``."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hkv", "d", "dtype", "page", "n_pages", "max_pages", "T",
+                                            "max_chunk", "frame")] + [("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int) for n in ("q_block", "n_select", "n_sink", "n_recent")] + \
+               [(n, _ll2) for n in ("q_stride", "o_stride", "k_stride", "v_stride")]
+
+    @classmethod
+    def make(cls, B, Hq, Hkv, d, *, page, n_pages, max_pages, T, max_chunk, frame=1, dtype=BF16, scale=0.0, q_block=0,
+             n_select=0, n_sink=0, n_recent=0):
+        return cls(B=B, Hq=Hq, Hkv=Hkv, d=d, dtype=_dtype_code(dtype), page=page, n_pages=n_pages,
+                   max_pages=max_pages, T=T, max_chunk=max_chunk, frame=frame, scale=scale, q_block=q_block,
+                   n_select=n_select, n_sink=n_sink, n_recent=n_recent)
+
+
 _P = ctypes.POINTER(Params)
+_R = ctypes.POINTER(RopeParams)
+_C = ctypes.POINTER(CacheParams)
+_sz = ctypes.c_size_t
 _sig = {
     "sparsepr_workspace_bytes": (ctypes.c_size_t, [_P]),
     "sparsepr_forward_workspace_bytes": (ctypes.c_size_t, [_P]),
@@ -98,6 +162,18 @@ _sig = {
     "sparsepr_dense_attention": (ctypes.c_int, [_P, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "sparsepr_workspace_error": (ctypes.c_int, [_P, _vp, _vp]),
     "sparsepr_workspace_clear_error": (ctypes.c_int, [_P, _vp, _vp]),
+    "sparsepr_rope_validate": (ctypes.c_int, [_R]),
+    "sparsepr_rope_frequencies": (ctypes.c_int, [_R, ctypes.POINTER(ctypes.c_double)]),
+    "sparsepr_rope": (ctypes.c_int, [_R] + [_vp] * 7),
+    "sparsepr_rope_backward": (ctypes.c_int, [_R] + [_vp] * 7),
+    "sparsepr_cache_validate": (ctypes.c_int, [_C]),
+    "sparsepr_paged_workspace_bytes": (_sz, [_C]),
+    "sparsepr_cache_append": (ctypes.c_int, [_C] + [_vp] * 8 + [_R, _vp, _vp, _vp, _sz, _vp]),
+    "sparsepr_select_units": (ctypes.c_int, [_C]),
+    "sparsepr_page_select": (ctypes.c_int, [_C] + [_vp] * 8 + [_sz, _vp]),
+    "sparsepr_paged_attention": (ctypes.c_int, [_C] + [_vp] * 11 + [_sz, _vp]),
+    "sparsepr_paged_error": (ctypes.c_int, [_vp, _vp]),
+    "sparsepr_paged_clear_error": (ctypes.c_int, [_vp, _vp]),
     "sparsepr_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "sparsepr_last_error": (ctypes.c_char_p, []),
     "sparsepr_last_launch_count": (ctypes.c_int, []),
@@ -325,3 +401,257 @@ def run_call(p: Params, Q, K, V, ws=None, trace=False):
         out["trace"] = ptr
         out["probe_trace"] = prt
     return out
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions and the paged K/V cache
+# ---------------------------------------------------------------------------
+# Tensors may be strided views (the last dimension contiguous): their strides go into a copy
+# of the params, so one params object serves calls with different layouts.  Shapes, types and
+# devices are checked here, because the library sees pointers only.
+def _expect(name, t, shape, dtypes, device=None):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if _type_name(t) not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(dtypes)}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _type_name(t):
+    return str(t.dtype).split(".")[-1]
+
+
+_NAMES = {BF16: "bfloat16", FP16: "float16", FP32: "float32"}
+
+
+def _elem(p):
+    if p.dtype not in _NAMES:
+        raise ValueError(f"unknown dtype code {p.dtype}")
+    return (_NAMES[p.dtype],)
+
+
+def _view(name, t, out, order):
+    """Element strides of the dimensions `order` of t into out; the rows must be contiguous."""
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    for i, d in enumerate(order):
+        # a dimension of one element has no stride of its own: take a contiguous one
+        out[i] = t.stride(d) if t.shape[d] > 1 else _packed(t, d)
+    if t.numel() and not any(out):     # all zero would mean contiguous to the library
+        raise ValueError(f"{name}: one row expanded over every dimension is not supported")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _packed(t, d):
+    n = 1
+    for i in range(d + 1, t.dim()):
+        n *= max(1, t.shape[i])
+    return n
+
+
+def _on(t):
+    """Launch on the tensor's device and its current stream."""
+    import torch
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    return torch.cuda.device(t.device)
+
+
+def sparsepr_rope_validate(p: RopeParams) -> int:
+    return _lib.sparsepr_rope_validate(ctypes.byref(p))
+
+
+def sparsepr_cache_validate(p: CacheParams) -> int:
+    return _lib.sparsepr_cache_validate(ctypes.byref(p))
+
+
+def sparsepr_rope_frequencies(p: RopeParams):
+    """Turns per position of every pair (float64 CPU tensor [rot_dim / 2])."""
+    import torch
+    n = max(0, p.rot_dim // 2)
+    buf = (ctypes.c_double * max(1, n))()
+    _check(_lib.sparsepr_rope_frequencies(ctypes.byref(p), buf), "sparsepr_rope_frequencies")
+    return torch.tensor(list(buf)[:n], dtype=torch.float64)
+
+
+def rope_frequencies(p: RopeParams, device):
+    """sparsepr_rope_frequencies on a device, as the calls take them; keep it with the params."""
+    return sparsepr_rope_frequencies(p).to(device)
+
+
+def _rope(fn, name, p, x, pos, freq, y, x2, y2):
+    _check(_lib.sparsepr_rope_validate(ctypes.byref(p)), name)
+    q = RopeParams.from_buffer_copy(p)
+    if (p.H2 > 0) != (x2 is not None) or (x2 is None) != (y2 is None):
+        raise ValueError("the second tensor goes with H2 > 0")
+    dev, el = x.device, _elem(p)
+    ptrs = []
+    for nm, t, h, out in (("x", x, p.H, q.x_stride), ("y", y, p.H, q.y_stride), ("x2", x2, p.H2, q.x2_stride),
+                          ("y2", y2, p.H2, q.y2_stride)):
+        if t is None:
+            ptrs.append(None)
+            continue
+        _expect(nm, t, (p.B, h, p.N, p.d), el, dev)
+        ptrs.append(_view(nm, t, out, (0, 1, 2)))
+    _expect("pos", pos, (p.n_axes, p.B, p.N) if p.pos_batched else (p.n_axes, p.N), ("int32",), dev)
+    _expect("freq", freq, (p.rot_dim // 2,), ("float64",), dev)
+    with _on(x):
+        _check(fn(ctypes.byref(q), ptrs[0], _ptr(pos), _ptr(freq), ptrs[1], ptrs[2], ptrs[3], _stream(x)), name)
+
+
+def sparsepr_rope(p: RopeParams, x, pos, freq, y, x2=None, y2=None):
+    """Rotates x [B, H, N, d] into y (and x2 [B, H2, N, d] into y2); strided views are allowed,
+    and y may be x.  pos int32 [n_axes, N] or, with pos_batched, [n_axes, B, N]."""
+    _rope(_lib.sparsepr_rope, "sparsepr_rope", p, x, pos, freq, y, x2, y2)
+
+
+def sparsepr_rope_backward(p: RopeParams, dy, pos, freq, dx, dy2=None, dx2=None):
+    """Gradient of sparsepr_rope: dx from dy (and dx2 from dy2)."""
+    _rope(_lib.sparsepr_rope_backward, "sparsepr_rope_backward", p, dy, pos, freq, dx, dy2, dx2)
+
+
+def sparsepr_paged_workspace_bytes(p: CacheParams) -> int:
+    return _lib.sparsepr_paged_workspace_bytes(ctypes.byref(p))
+
+
+def paged_workspace(p: CacheParams, device):
+    """A workspace for the paged calls, its error word cleared.  Concurrent calls need one each."""
+    import torch
+    n = sparsepr_paged_workspace_bytes(p)
+    if n == 0:
+        _check(sparsepr_cache_validate(p), "workspace size")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def sparsepr_paged_error(ws) -> int:
+    with _on(ws):
+        return _lib.sparsepr_paged_error(_ptr(ws), _stream(ws))
+
+
+def sparsepr_paged_clear_error(ws):
+    with _on(ws):
+        _check(_lib.sparsepr_paged_clear_error(_ptr(ws), _stream(ws)), "sparsepr_paged_clear_error")
+
+
+def sparsepr_select_units(p: CacheParams) -> int:
+    """Most selection units of a call with these params (rows of sel and sel_count)."""
+    n = _lib.sparsepr_select_units(ctypes.byref(p))
+    if n < 0:
+        _check(sparsepr_cache_validate(p), "sparsepr_select_units")
+        raise ValueError("sparsepr_select_units needs n_select >= 1")
+    return n
+
+
+def alloc_selection(p: CacheParams, device):
+    """sel [units, Hkv, n_select] and sel_count [units, Hkv] for sparsepr_page_select."""
+    import torch
+    u = sparsepr_select_units(p)
+    return (torch.empty(u, p.Hkv, p.n_select, dtype=torch.int32, device=device),
+            torch.empty(u, p.Hkv, dtype=torch.int32, device=device))
+
+
+def alloc_cache(p: CacheParams, device):
+    """k_pages, v_pages [n_pages, Hkv, page, d] and k_mean [n_pages, Hkv, d]."""
+    import torch
+    dt = torch.float16 if p.dtype == FP16 else torch.bfloat16
+    shape = (p.n_pages, p.Hkv, p.page, p.d)
+    return dict(k_pages=torch.empty(shape, dtype=dt, device=device),
+                v_pages=torch.empty(shape, dtype=dt, device=device),
+                k_mean=torch.empty(p.n_pages, p.Hkv, p.d, dtype=dt, device=device))
+
+
+def _sequences(p, dev, q_start, kv_len, page_table, ws):
+    i32 = ("int32",)
+    _expect("q_start", q_start, (p.B + 1,), i32, dev)
+    _expect("kv_len", kv_len, (p.B,), i32, dev)
+    _expect("page_table", page_table, (p.B, p.max_pages), i32, dev)
+    _expect("ws", ws, (ws.numel(),), ("uint8",), dev)
+
+
+def _pages(p, dev, **tensors):
+    for nm, t in tensors.items():
+        _expect(nm, t, (p.n_pages, p.Hkv, p.d) if nm == "k_mean" else (p.n_pages, p.Hkv, p.page, p.d), _elem(p), dev)
+
+
+def sparsepr_cache_append(p: CacheParams, K, V, q_start, kv_len, page_table, k_pages, v_pages, k_mean, ws, rope=None,
+                          pos=None, freq=None):
+    """Writes the new rows K, V [T, Hkv, d] into their page slots and the touched pages' mean
+    keys; with rope (RopeParams) the keys are rotated by pos int32 [n_axes, T] on the way."""
+    _check(sparsepr_cache_validate(p), "sparsepr_cache_append")
+    q, dev, el = CacheParams.from_buffer_copy(p), K.device, _elem(p)
+    _expect("K", K, (p.T, p.Hkv, p.d), el, dev)
+    _expect("V", V, (p.T, p.Hkv, p.d), el, dev)
+    _sequences(p, dev, q_start, kv_len, page_table, ws)
+    _pages(p, dev, k_pages=k_pages, v_pages=v_pages, k_mean=k_mean)
+    if rope is not None:
+        if pos is None or freq is None:
+            raise ValueError("rope needs pos and freq")
+        _expect("pos", pos, (rope.n_axes, p.T), ("int32",), dev)
+        _expect("freq", freq, (rope.rot_dim // 2,), ("float64",), dev)
+    kp, vp = _view("K", K, q.k_stride, (0, 1)), _view("V", V, q.v_stride, (0, 1))
+    with _on(K):
+        _check(_lib.sparsepr_cache_append(ctypes.byref(q), kp, vp, _ptr(q_start), _ptr(kv_len), _ptr(page_table),
+                                          _ptr(k_pages), _ptr(v_pages), _ptr(k_mean),
+                                          None if rope is None else ctypes.byref(rope),
+                                          None if rope is None else _ptr(pos), None if rope is None else _ptr(freq),
+                                          _ptr(ws), ws.numel(), _stream(K)), "sparsepr_cache_append")
+
+
+def sparsepr_page_select(p: CacheParams, Q, q_start, kv_len, page_table, k_mean, sel, sel_count, ws):
+    """Page lists of every unit of q_block tokens and key/value head, by mean query . mean key."""
+    units = sparsepr_select_units(p)
+    q, dev = CacheParams.from_buffer_copy(p), Q.device
+    _expect("Q", Q, (p.T, p.Hq, p.d), _elem(p), dev)
+    _sequences(p, dev, q_start, kv_len, page_table, ws)
+    _pages(p, dev, k_mean=k_mean)
+    _expect("sel", sel, (units, p.Hkv, p.n_select), ("int32",), dev)
+    _expect("sel_count", sel_count, (units, p.Hkv), ("int32",), dev)
+    qp = _view("Q", Q, q.q_stride, (0, 1))
+    with _on(Q):
+        _check(_lib.sparsepr_page_select(ctypes.byref(q), qp, _ptr(q_start), _ptr(kv_len), _ptr(page_table),
+                                         _ptr(k_mean), _ptr(sel), _ptr(sel_count), _ptr(ws), ws.numel(), _stream(Q)),
+               "sparsepr_page_select")
+
+
+def sparsepr_paged_attention(p: CacheParams, Q, q_start, kv_len, page_table, k_pages, v_pages, O, lse, ws, sel=None,
+                             sel_count=None):
+    """Attention of the new tokens Q [T, Hq, d] over the cache into O (and lse float32 [T, Hq] or
+    None); with sel and sel_count over the pages of their lists."""
+    _check(sparsepr_cache_validate(p), "sparsepr_paged_attention")
+    q, dev, el = CacheParams.from_buffer_copy(p), Q.device, _elem(p)
+    _expect("Q", Q, (p.T, p.Hq, p.d), el, dev)
+    _expect("O", O, (p.T, p.Hq, p.d), el, dev)
+    if lse is not None:
+        _expect("lse", lse, (p.T, p.Hq), ("float32",), dev)
+    _sequences(p, dev, q_start, kv_len, page_table, ws)
+    _pages(p, dev, k_pages=k_pages, v_pages=v_pages)
+    if (sel is None) != (sel_count is None):
+        raise ValueError("sel and sel_count come together")
+    if sel is not None:
+        units = sparsepr_select_units(p)
+        _expect("sel", sel, (units, p.Hkv, p.n_select), ("int32",), dev)
+        _expect("sel_count", sel_count, (units, p.Hkv), ("int32",), dev)
+    qp, op = _view("Q", Q, q.q_stride, (0, 1)), _view("O", O, q.o_stride, (0, 1))
+    with _on(Q):
+        _check(_lib.sparsepr_paged_attention(ctypes.byref(q), qp, _ptr(q_start), _ptr(kv_len), _ptr(page_table),
+                                             _ptr(k_pages), _ptr(v_pages), _ptr(sel), _ptr(sel_count), op, _ptr(lse),
+                                             _ptr(ws), ws.numel(), _stream(Q)), "sparsepr_paged_attention")
+
+
+def rollout_step(p: CacheParams, cache, Q, K, V, q_start, kv_len, page_table, O, ws, rope=None, pos=None, freq=None,
+                 selection=None, lse=None):
+    """One step of a rollout on the current stream: K and V (rotated with rope) are appended to
+    cache (alloc_cache), then Q attends to it, through the page lists of selection
+    (alloc_selection) when given.  Q is rotated by the caller (sparsepr_rope)."""
+    sparsepr_cache_append(p, K, V, q_start, kv_len, page_table, cache["k_pages"], cache["v_pages"], cache["k_mean"],
+                          ws, rope=rope, pos=pos, freq=freq)
+    sel = cnt = None
+    if selection is not None:
+        sel, cnt = selection
+        sparsepr_page_select(p, Q, q_start, kv_len, page_table, cache["k_mean"], sel, cnt, ws)
+    sparsepr_paged_attention(p, Q, q_start, kv_len, page_table, cache["k_pages"], cache["v_pages"], O, lse, ws, sel=sel,
+                             sel_count=cnt)
+    return O

@@ -1,0 +1,276 @@
+// Shared pieces of the paged-cache kernels: element types, the call's arguments, and the
+// mapping of work items to sequences.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace spr {
+namespace paged {
+
+// ---------------------------------------------------------------------------
+// 16-bit element types (packed pairs in 32-bit words, low half first)
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);   // round to nearest even
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <typename T>
+__device__ __forceinline__ float as_f32(T x);
+template <>
+__device__ __forceinline__ float as_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float as_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float as_f32<__half>(__half x) { return __half2float(x); }
+
+// The probabilities enter the second product as 16-bit values.  fp16 has no room below
+// 2^-24, so they are kept 2^kShift higher there (at most 2^15 with the sum bound below);
+// a key 2^-31 below the row's largest then still counts.  bf16 has fp32's range.
+template <typename T>
+struct ProbShift;
+template <>
+struct ProbShift<__nv_bfloat16> {
+  static constexpr float v = 0.f;
+};
+template <>
+struct ProbShift<__half> {
+  static constexpr float v = 7.f;
+};
+
+// ---------------------------------------------------------------------------
+// Arguments of the attention kernels
+// ---------------------------------------------------------------------------
+struct Args {
+  const void* Q;
+  const int* q_start;
+  const int* kv_len;
+  const int* table;
+  const int* sel;        // NULL: the whole cache
+  const int* sel_cnt;
+  void* O;
+  float* lse;
+  float* part_o;         // [S][T * Hq][d] of split units
+  float* part_lse;       // [S][T * Hq]
+  int* err;
+  int B, Hq, Hkv, G, page, n_pages, max_pages, T, max_chunk, frame;
+  int q_block, n_select;
+  int ppu;               // row parts per unit (selection, tensor-tile kernel), else 1
+  int items;             // upper bound of the (sequence, unit, part) items of a head
+  int S, min_split;      // most splits of an item's key stream, fewest tiles of a split
+  float scale_log2;
+  long long qst, qsh, ost, osh;
+};
+
+// One sequence's token range and cache length, with whatever the caller's arrays hold
+// brought into bounds (bad: something had to be).
+struct Seq {
+  int b, q0, n, len;
+  bool bad;
+};
+
+__device__ __forceinline__ Seq load_seq(const Args& a, int b) {
+  Seq s;
+  s.b = b;
+  const int lo = a.q_start[b], hi = a.q_start[b + 1], len = a.kv_len[b];
+  const int cap = a.max_pages * a.page;
+  s.q0 = min(max(lo, 0), a.T);
+  s.n = max(0, min(hi, a.T) - s.q0);
+  s.len = min(max(len, 0), cap);
+  s.bad = lo < 0 || hi > a.T || hi < lo || len != s.len || s.n > a.max_chunk;
+  return s;
+}
+
+// Items of a sequence with n new tokens.  Kinds: kWhole one item per sequence, kRows
+// ceil(n G / rows) parts of the whole sequence, kUnits ceil(n / q_block) units of ppu parts.
+enum ItemKind { kWhole = 0, kRows = 1, kUnits = 2 };
+
+template <int KIND>
+__device__ __forceinline__ int item_count(int n, int G, int rows, int q_block, int ppu) {
+  if (KIND == kWhole) return 1;
+  if (KIND == kRows) return (int)(((long long)n * G + rows - 1) / rows);
+  return (int)(((long long)n + q_block - 1) / q_block) * ppu;
+}
+
+// Sequence and rank of item `idx` (counted sequence by sequence); every thread of the block
+// calls it, all get the result; b = -1 past the last item.  Each thread takes a run of
+// sequences, their counts are scanned, and the run that holds idx is walked by its thread.
+template <int KIND, int NT>
+__device__ __forceinline__ int2 find_item(const int* __restrict__ q_start, int B, int T, int idx, int G, int rows,
+                                          int q_block, int ppu, int* sm /* [NT / 32 + 2] */) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (KIND == kWhole) return make_int2(idx < B ? idx : -1, 0);
+  const int run = (B + NT - 1) / NT;
+  const int b0 = min(B, tid * run), b1 = min(B, b0 + run);
+  auto count = [&](int b) -> int {
+    const int lo = min(max(q_start[b], 0), T);
+    return item_count<KIND>(max(0, min(q_start[b + 1], T) - lo), G, rows, q_block, ppu);
+  };
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += count(b);
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sm[warp] = inc;
+  if (tid == 0) {
+    sm[NT / 32] = -1;
+    sm[NT / 32 + 1] = 0;
+  }
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += sm[w];
+  int at = base + inc - mine;
+  if (idx >= at && idx < at + mine) {
+    for (int b = b0; b < b1; ++b) {
+      const int c = count(b);
+      if (idx < at + c) {
+        sm[NT / 32] = b;
+        sm[NT / 32 + 1] = idx - at;
+        break;
+      }
+      at += c;
+    }
+  }
+  __syncthreads();
+  return make_int2(sm[NT / 32], sm[NT / 32 + 1]);
+}
+
+// Keys [0, end) that a token at position pos may see.
+__device__ __forceinline__ int visible_end(int pos, int frame, int len) {
+  if (frame == 0) return len;
+  if (pos < 0) return 0;
+  const long long e = ((long long)(pos / frame) + 1) * frame;
+  return e < len ? (int)e : len;
+}
+
+// The keys of an item form a stream: the cache in order, or the pages of its list in order.
+// Everything a token may see is a prefix of that stream, because pages ascend; its length
+// for the visible range [0, end):
+__device__ __forceinline__ int stream_limit(int end, const int* __restrict__ list, int cnt, int page,
+                                           int* entries = nullptr) {
+  if (!list) return end;
+  int lo = 0, hi = cnt;            // entries whose page starts below `end`
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((long long)list[mid] * page < end) lo = mid + 1; else hi = mid;
+  }
+  if (entries) *entries = lo;
+  if (lo == 0) return 0;
+  const long long in = (long long)end - (long long)list[lo - 1] * page;
+  return (lo - 1) * page + (int)(in < 0 ? 0 : in < page ? in : page);
+}
+
+// Splits of an item whose stream has `tiles` tiles: split s of ns takes
+// [tiles s / ns, tiles (s + 1) / ns).
+__device__ __forceinline__ int split_count(int tiles, int S, int min_split) {
+  const int n = (tiles + min_split - 1) / min_split;
+  return n < 1 ? 1 : (n < S ? n : S);
+}
+__device__ __forceinline__ int split_at(int tiles, int s, int ns) { return (int)((long long)tiles * s / ns); }
+
+}  // namespace paged
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+struct RopeArgs {
+  const void* x[2];
+  void* y[2];
+  long long xs[2][3], ys[2][3];   // batch, head, token strides (elements)
+  int B, N, H[2], d, rot, layout, n_axes, axis_pairs[3], pos_batched, dtype;
+  float mag, sign;
+  const int* pos;
+  const double* freq;
+  bool vec;                       // 16-byte accesses allowed
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+
+struct AppendArgs {
+  const void* K;
+  const void* V;
+  const int* q_start;
+  const int* kv_len;
+  const int* table;
+  void* kp;
+  void* vp;
+  void* km;
+  const int* pos;                 // NULL: no rotation
+  const double* freq;
+  int* err;
+  int B, Hkv, d, dtype, page, n_pages, max_pages, T;
+  int rot, layout, n_axes, axis_pairs[3];
+  float mag;
+  long long kst, ksh, vst, vsh;
+};
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
+
+struct SelectArgs {
+  const void* Q;
+  const int* q_start;
+  const int* kv_len;
+  const int* table;
+  const void* km;
+  int* sel;
+  int* cnt;
+  unsigned long long* keys;       // [units][Hkv][max_pages], used when `keys_global`
+  int* err;
+  int B, Hq, Hkv, d, dtype, page, n_pages, max_pages, T, frame, q_block, n_select, n_sink, n_recent;
+  int units, splits;
+  bool keys_global;
+  long long qst, qsh;
+};
+struct SelectPlan {
+  int splits;
+  bool keys_global;
+};
+SelectPlan select_plan(int units, int Hkv, int max_pages);
+cudaError_t launch_page_select(const SelectArgs& a, int* launches, cudaStream_t st);
+
+// rows kernel: items of at most 16 * mt query rows on mma.sync; tile kernel: 256-row items on
+// tcgen05; combine: the join of split items.
+struct PagedPlan {
+  bool rows;        // rows kernel, else tile kernel
+  int mt;           // 16-row tiles of the rows kernel
+  int kind;         // paged::ItemKind
+  int ppu, items, S, min_split;
+};
+PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int max_chunk, int q_block, bool sel);
+cudaError_t launch_paged_rows(const paged::Args& a, const PagedPlan& pl, int d, int dtype, const void* kp,
+                              const void* vp, cudaStream_t st);
+cudaError_t launch_paged_tiles(const paged::Args& a, const PagedPlan& pl, int d, int dtype, const void* kp,
+                               const void* vp, cudaStream_t st);
+cudaError_t launch_paged_combine(const paged::Args& a, const PagedPlan& pl, int d, int dtype, cudaStream_t st);
+constexpr int kPagedTileRows = 256;   // query rows of an item of the tile kernel
+constexpr int kPagedRowsBN = 64;      // keys of a tile of the rows kernel
+constexpr int kPagedTileBN = 128;     // keys of a chunk of the tile kernel
+
+}  // namespace spr

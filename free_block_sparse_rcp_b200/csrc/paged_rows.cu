@@ -1,0 +1,548 @@
+// Attention of few query rows over the paged cache (single tokens, short chunks), and the join
+// of split items.
+//
+// An item is the new tokens of one sequence (or of one unit with its page list) and the query
+// heads of one key/value head: at most 32 rows, which share one stream of keys.  The work is
+// reading that stream: 4 d bytes per key for 4 d rows operations, so the kernel is built to
+// keep memory busy and uses the small warp-wide matrix product (16 x 8 x 16); a 128-row
+// tensor-core tile would be mostly padding here.
+//   producer warp   TMA boxes of min(page, 64) rows, 64 keys of K and V per stage
+//   4 MT warps      warp (mt, slice) takes 16 query rows and 16 of the stage's 64 keys, keeps
+//                   its own running maximum, sum and O in registers; the four slices are joined
+//                   at the end through shared memory
+// Long streams are cut into splits (grid z); a split writes its normalised O and lse in fp32,
+// and k_paged_combine joins them.
+#include <cuda.h>
+
+#include "kernels.h"
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace spr {
+namespace paged {
+
+using namespace spr::tc;
+
+constexpr int BNR = kPagedRowsBN;
+
+template <int D>
+struct RowsCfg {
+  static constexpr int ST = D == 128 ? 3 : 6;                  // stages: two CTAs per SM
+  static constexpr uint32_t kTile = (uint32_t)BNR * D * 2;     // bytes of K (or V) of a stage
+  static constexpr uint32_t kBytes = ST * 2 * kTile;
+};
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// What an item reads, computed alike by the attention and the join.
+struct Item {
+  Seq s;
+  int tok0, ntok;          // tokens of the sequence in this item
+  const int* list;         // page list (NULL: the whole cache)
+  int cnt, total;          // list entries; keys of the stream
+  bool bad;
+};
+
+template <int KIND, int NT>
+__device__ __forceinline__ bool load_item(const Args& a, int idx, int h, int* sm, Item& it) {
+  const int2 f = find_item<KIND, NT>(a.q_start, a.B, a.T, idx, a.G, 0, a.q_block, 1, sm);
+  if (f.x < 0) return false;
+  it.s = load_seq(a, f.x);
+  it.bad = it.s.bad;
+  it.list = nullptr;
+  it.cnt = 0;
+  if (KIND == kUnits) {
+    it.tok0 = f.y * a.q_block;
+    it.ntok = min(a.q_block, it.s.n - it.tok0);
+    const size_t at = (size_t)idx * a.Hkv + h;
+    it.list = a.sel + at * a.n_select;
+    const int c = a.sel_cnt[at];
+    it.cnt = min(max(c, 0), a.n_select);
+    it.bad |= c != it.cnt;
+  } else {
+    it.tok0 = 0;
+    it.ntok = it.s.n;
+  }
+  if (it.ntok <= 0) return false;
+  const int end = visible_end(it.s.len - it.s.n + it.tok0 + it.ntok - 1, a.frame, it.s.len);
+  int seen = it.cnt;
+  it.total = stream_limit(end, it.list, it.cnt, a.page, &seen);
+  it.bad |= seen != it.cnt;      // the unit's last token sees every page of its list
+  return true;
+}
+
+// Page of stream row p (a multiple of the box height), checked: -1 if it may not be read.
+__device__ __forceinline__ int stream_page(const Args& a, const Item& it, int p) {
+  int j = p / a.page;
+  if (it.list) {
+    const int k = j;
+    j = it.list[k];
+    // lists ascend strictly and stay within the sequence
+    if (j < 0 || (long long)j * a.page >= it.s.len || (k > 0 && it.list[k - 1] >= j)) return -1;
+  }
+  const int pid = a.table[(size_t)it.s.b * a.max_pages + j];
+  return pid >= 0 && pid < a.n_pages ? pid : -1;
+}
+
+template <typename T, int D, int MT, int KIND>
+__global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_constant__ CUtensorMap tmk,
+                                                              const __grid_constant__ CUtensorMap tmv, Args a) {
+  using C = RowsCfg<D>;
+  constexpr int NT = 128 * MT + 32, NW = 4 * MT, ST = C::ST;
+  constexpr float SHIFT = ProbShift<T>::v;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ uint64_t s_full[ST], s_empty[ST];
+  __shared__ int s_abort, s_bad, s_find[NT / 32 + 2];
+  __shared__ float s_m[MT][4][16], s_l[MT][4][16];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int idx = blockIdx.x, h = blockIdx.y;
+  const uint32_t base = su32(smem);
+  if (base & 1023u) {
+    if (tid == 0) set_error(a.err, DERR_INDEX);
+    return;
+  }
+  Item it;
+  if (!load_item<KIND, NT>(a, idx, h, s_find, it)) return;
+  const int tiles = (it.total + BNR - 1) / BNR;
+  const int ns = split_count(tiles, a.S, a.min_split);
+  if ((int)blockIdx.z >= ns) return;
+  const int t0 = split_at(tiles, blockIdx.z, ns), t1 = split_at(tiles, blockIdx.z + 1, ns);
+  if (tid == 0) {
+    s_abort = 0;
+    s_bad = it.bad ? 1 : 0;
+    if (it.bad) set_error(a.err, DERR_INDEX);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(su32(&s_full[i]), 1);
+      mbar_init(su32(&s_empty[i]), NW);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int nrows = min(it.ntok * a.G, 16 * MT);
+
+  if (warp == NW) {
+    // ---------------- producer ----------------
+    const int box = min(a.page, BNR), boxes = BNR / box;          // boxes of a tile
+    const int jobs = boxes * (D / 64) * 2;                        // box x column half x {K, V}; <= 16
+    const int bx = lane / (D / 64 * 2), rest = lane % (D / 64 * 2), half = rest >> 1, isv = rest & 1;
+    bool ok = true;
+    int pid = 0, issued = 0;
+    auto fetch = [&](int t) -> int {
+      const int p = t * BNR + bx * box;
+      return lane < jobs && t < t1 && p < it.total ? stream_page(a, it, p) : -2;
+    };
+    pid = fetch(t0);
+    for (int t = t0; t < t1; ++t) {
+      const int i = t - t0, st = i % ST;
+      const int next = fetch(t + 1);
+      if (lane == 0) ok = i < ST || bounded_wait(su32(&s_empty[st]), ((i / ST) - 1) & 1, &s_abort, a.err);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      if (pid == -1) {           // the rows become NaN; the load is replaced by a page that exists
+        s_bad = 1;
+        set_error(a.err, DERR_INDEX);
+        pid = 0;
+      }
+      __syncwarp();
+      const unsigned go = __ballot_sync(0xffffffffu, pid >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(su32(&s_full[st]), (uint32_t)__popc(go) * box * 128);
+      __syncwarp();
+      if (pid >= 0) {
+        const int sub = (t * BNR + bx * box) % a.page;
+        const uint32_t dst = base + st * 2 * C::kTile + isv * C::kTile + half * (BNR * 128) + bx * box * 128;
+        tma_load_2d(dst, isv ? &tmv : &tmk, 64 * half, (pid * a.Hkv + h) * a.page + sub, su32(&s_full[st]));
+      }
+      pid = next;
+      issued = i + 1;
+    }
+    // a wait that ran out: let the loads in flight land before the block ends
+    if (!ok && lane == 0)
+      for (int i = issued > ST ? issued - ST : 0; i < issued; ++i) drain_wait(su32(&s_full[i % ST]), (i / ST) & 1);
+    __syncwarp();
+  } else {
+    // ---------------- 16 rows x 16-key slices ----------------
+    const int mt = warp >> 2, sl = warp & 3;
+    const int g = lane >> 2, q2 = (lane & 3) * 2;
+    uint32_t qf[D / 16][4];
+    int lim[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = mt * 16 + g + 8 * r;
+      const bool in = row < nrows;
+      const int tok = in ? row / a.G : 0, gh = in ? row - tok * a.G : 0;
+      const T* qp = (const T*)a.Q + (long long)(it.s.q0 + it.tok0 + tok) * a.qst + (long long)(h * a.G + gh) * a.qsh;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[k][r] = in ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + q2) : 0u;
+        qf[k][2 + r] = in ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8 + q2) : 0u;
+      }
+      lim[r] = it.total;
+      if (in && a.frame != 0) {
+        const int e = visible_end(it.s.len - it.s.n + it.tok0 + tok, a.frame, it.s.len);
+        lim[r] = min(it.total, stream_limit(e, it.list, it.cnt, a.page));
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    bool ok = true;
+    // K fragments: matrices (keys 0-7, k 0-7), (keys 0-7, k 8-15), (keys 8-15, k 0-7), (keys 8-15, k 8-15)
+    const int kr = sl * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, kc = (lane >> 3) & 1;
+    // V fragments: matrices (keys 0-7, n 0-7), (keys 8-15, n 0-7), (keys 0-7, n 8-15), (keys 8-15, n 8-15)
+    const int vr = sl * 16 + (lane & 15), vc = lane >> 4;
+    for (int t = t0; t < t1; ++t) {
+      const int i = t - t0, st = i % ST;
+      ok = __all_sync(0xffffffffu, bounded_wait(su32(&s_full[st]), (i / ST) & 1, &s_abort, a.err));
+      if (!ok) break;
+      const uint32_t sk = base + st * 2 * C::kTile, sv = sk + C::kTile;
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        ldsm4(b, sk + tile_off(kr, 2 * k + kc, BNR));
+        mma16816<T>(s[0], qf[k], b[0], b[1]);
+        mma16816<T>(s[1], qf[k], b[2], b[3]);
+      }
+      const int k0 = t * BNR + sl * 16;     // stream row of the slice's first key
+      const bool edge = __any_sync(0xffffffffu, k0 + 16 > min(lim[0], lim[1]));
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[n][e] * a.scale_log2;
+          if (edge && k0 + n * 8 + q2 + (e & 1) >= lim[e >> 1]) x = -INFINITY;
+          s[n][e] = x;
+          mx[e >> 1] = fmaxf(mx[e >> 1], x);
+        }
+      bool moved = false;
+      float mu[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        moved |= mx[r] > m[r];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mn = fmaxf(m[r], mx[r]);
+          const float al = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn);
+          m[r] = mn;
+          l[r] *= al;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[n][2 * r] *= al;
+            o[n][2 * r + 1] *= al;
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) mu[r] = m[r] == -INFINITY ? 0.f : m[r] - SHIFT;
+      uint32_t pf[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float p0 = ex2(s[n][2 * r] - mu[r]), p1 = ex2(s[n][2 * r + 1] - mu[r]);
+          l[r] += p0 + p1;
+          pf[2 * n + r] = pack2<T>(p0, p1);
+        }
+      const bool tail = k0 + 16 > it.total;   // value rows past the stream may hold anything
+      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+      if (tail) {
+        const int left = it.total - k0 - q2;   // this thread's keys q2, q2 + 1, q2 + 8, q2 + 9
+        keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+        keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
+      }
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        uint32_t b[4];
+        ldsm4t(b, sv + tile_off(vr, 2 * n + vc, BNR));
+        if (tail) {
+          b[0] &= keep0;
+          b[1] &= keep1;
+          b[2] &= keep0;
+          b[3] &= keep1;
+        }
+        mma16816<T>(o[2 * n], pf, b[0], b[1]);
+        mma16816<T>(o[2 * n + 1], pf, b[2], b[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(su32(&s_empty[st]));
+    }
+    // ---------------- join of the four slices ----------------
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if ((lane & 3) == 0) {
+        s_m[mt][sl][g + 8 * r] = m[r];
+        s_l[mt][sl][g + 8 * r] = l[r];
+      }
+    }
+    named_sync(1 + mt, 128);
+    float ms[2], ls[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, s_m[mt][w][g + 8 * r]);
+      float ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float mw = s_m[mt][w][g + 8 * r];
+        if (mw != -INFINITY) ll += s_l[mt][w][g + 8 * r] * ex2(mw - mm);
+      }
+      ms[r] = mm;
+      ls[r] = ll;
+      const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - mm);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][2 * r] *= f;
+        o[n][2 * r + 1] *= f;
+      }
+    }
+    // every stage has landed and been read by all warps of all row tiles: the buffers are free
+    // (slices 1-3 of a row tile use 3 x 16 x D x 4 bytes)
+    named_sync(15, 128 * MT);
+    float4* buf = reinterpret_cast<float4*>(smem) + (size_t)mt * 3 * (D / 8) * 32;
+    if (sl > 0) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        buf[((size_t)(sl - 1) * (D / 8) + n) * 32 + lane] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+    }
+    named_sync(1 + mt, 128);
+    if (sl == 0) {
+      const bool poison = !ok || s_bad != 0 || s_abort != 0;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = mt * 16 + g + 8 * r;
+        float inv = ls[r] > 0.f ? 1.f / ls[r] : 0.f;
+        float z = ls[r] > 0.f ? (ms[r] - SHIFT + log2f(ls[r])) * 0.69314718055994531f : -INFINITY;
+        if (!(ls[r] == ls[r]) || poison) inv = z = __int_as_float(0x7fffffff);
+        const int tok = row / a.G, gh = row - tok * a.G;
+        const long long qrow = it.s.q0 + it.tok0 + tok;
+        const int qh = h * a.G + gh;
+        const bool in = row < nrows;
+        const size_t prow = ((size_t)blockIdx.z * a.T + (in ? qrow : 0)) * a.Hq + qh;
+        T* op = (T*)a.O + (in ? qrow : 0) * a.ost + (long long)qh * a.osh;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          float x = o[n][2 * r], y = o[n][2 * r + 1];
+#pragma unroll
+          for (int w = 0; w < 3; ++w) {
+            const float4 v = buf[((size_t)w * (D / 8) + n) * 32 + lane];
+            x += r ? v.z : v.x;
+            y += r ? v.w : v.y;
+          }
+          if (in) {
+            if (ns > 1) *reinterpret_cast<float2*>(a.part_o + prow * D + n * 8 + q2) = make_float2(x * inv, y * inv);
+            else *reinterpret_cast<uint32_t*>(op + n * 8 + q2) = pack2<T>(x * inv, y * inv);
+          }
+        }
+        if (in && (lane & 3) == 0) {
+          if (ns > 1) a.part_lse[prow] = z;
+          else if (a.lse) a.lse[qrow * a.Hq + qh] = z;
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Join of split items: grid (items, Hkv), rows of the item dealt to the block's warps.
+//   O = sum_s exp(lse_s - lse) O_s,  lse = ln sum_s exp(lse_s)
+// ---------------------------------------------------------------------------
+constexpr int kCombThreads = 256;
+
+template <typename T, int D, int KIND>
+__global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int rows_per_item, int bn) {
+  __shared__ int s_find[kCombThreads / 32 + 2];
+  const int idx = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Item it;
+  int row0 = 0, nrows;
+  if (KIND == kRows) {      // parts of whole sequences (tile kernel)
+    const int2 f = find_item<kRows, kCombThreads>(a.q_start, a.B, a.T, idx, a.G, rows_per_item, 1, 1, s_find);
+    if (f.x < 0) return;
+    it.s = load_seq(a, f.x);
+    it.tok0 = 0;
+    row0 = f.y * rows_per_item;
+    nrows = (int)min((long long)rows_per_item, (long long)it.s.n * a.G - row0);
+    const int last = (row0 + nrows - 1) / a.G;
+    it.total = visible_end(it.s.len - it.s.n + last, a.frame, it.s.len);
+  } else {
+    const int unit = idx / a.ppu, part = idx - unit * a.ppu;
+    if (!load_item<KIND, kCombThreads>(a, unit, h, s_find, it)) return;
+    row0 = part * rows_per_item;
+    nrows = min(rows_per_item, it.ntok * a.G - row0);
+    if (nrows <= 0) return;
+    if (a.ppu > 1 || KIND == kUnits) {
+      const int last = it.tok0 + (row0 + nrows - 1) / a.G;
+      it.total = stream_limit(visible_end(it.s.len - it.s.n + last, a.frame, it.s.len), it.list, it.cnt, a.page);
+    }
+  }
+  const int ns = split_count((it.total + bn - 1) / bn, a.S, a.min_split);
+  if (ns <= 1) return;
+  for (int r = warp; r < nrows; r += kCombThreads / 32) {
+    const int tok = (row0 + r) / a.G, qh = h * a.G + (row0 + r - tok * a.G);
+    const size_t qrow = (size_t)it.s.q0 + it.tok0 + tok, prow = qrow * a.Hq + qh, step = (size_t)a.T * a.Hq;
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int s = lane; s < ns; s += 32) {
+      const float z = a.part_lse[prow + s * step];
+      nan |= !(z == z);
+      mx = fmaxf(mx, z);
+    }
+    mx = warp_max(mx);
+    nan = __any_sync(0xffffffffu, nan);
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    float den = 0.f;
+    float acc[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+    for (int s = 0; s < ns; ++s) {
+      const float w = expf(a.part_lse[prow + s * step] - mu);
+      den += w;
+      const float* po = a.part_o + (prow + s * step) * D + lane * (D / 32);
+      if constexpr (D == 128) {
+        const float4 v = *reinterpret_cast<const float4*>(po);
+        acc[0] += w * v.x;
+        acc[1] += w * v.y;
+        acc[2] += w * v.z;
+        acc[3] += w * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(po);
+        acc[0] += w * v.x;
+        acc[1] += w * v.y;
+      }
+    }
+    nan |= !(den == den);
+    const float inv = nan ? __int_as_float(0x7fffffff) : (den > 0.f ? 1.f / den : 0.f);
+    T* op = (T*)a.O + (long long)qrow * a.ost + (long long)qh * a.osh + lane * (D / 32);
+#pragma unroll
+    for (int i = 0; i < D / 32; i += 2)
+      *reinterpret_cast<uint32_t*>(op + i) = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[prow] = nan ? __int_as_float(0x7fffffff) : (den > 0.f ? mu + logf(den) : -INFINITY);
+  }
+}
+
+}  // namespace paged
+
+namespace {
+
+template <typename T, int D, int MT, int KIND>
+cudaError_t rows_t(const paged::Args& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  auto kern = paged::k_paged_rows<T, D, MT, KIND>;
+  const size_t sm = paged::RowsCfg<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(a.items, a.Hkv, a.S), 128 * MT + 32, sm, st>>>(tk, tv, a);
+  return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t rows_d(const paged::Args& a, const PagedPlan& pl, const CUtensorMap& tk, const CUtensorMap& tv,
+                   cudaStream_t st) {
+  if (pl.kind == paged::kUnits)
+    return pl.mt == 1 ? rows_t<T, D, 1, paged::kUnits>(a, tk, tv, st) : rows_t<T, D, 2, paged::kUnits>(a, tk, tv, st);
+  return pl.mt == 1 ? rows_t<T, D, 1, paged::kWhole>(a, tk, tv, st) : rows_t<T, D, 2, paged::kWhole>(a, tk, tv, st);
+}
+
+template <typename T, int D>
+cudaError_t combine_t(const paged::Args& a, const PagedPlan& pl, cudaStream_t st) {
+  const dim3 grid(a.items, a.Hkv);
+  const int rows = pl.rows ? 16 * pl.mt : kPagedTileRows, bn = pl.rows ? kPagedRowsBN : kPagedTileBN;
+  if (pl.kind == paged::kUnits) paged::k_paged_combine<T, D, paged::kUnits><<<grid, paged::kCombThreads, 0, st>>>(a, rows, bn);
+  else if (pl.kind == paged::kRows) paged::k_paged_combine<T, D, paged::kRows><<<grid, paged::kCombThreads, 0, st>>>(a, rows, bn);
+  else paged::k_paged_combine<T, D, paged::kWhole><<<grid, paged::kCombThreads, 0, st>>>(a, rows, bn);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Rows of an item: the unit's (or the longest sequence's) tokens times the heads that share a
+// key/value head.  Up to 32 go to the rows kernel, more to the 256-row tensor tiles.
+PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int max_chunk, int q_block, bool sel) {
+  PagedPlan p{};
+  const long long G = Hq / Hkv;
+  const long long tok = sel && q_block < max_chunk ? q_block : max_chunk;
+  const long long rows = tok * G;
+  p.rows = rows <= 32;
+  p.mt = rows <= 16 ? 1 : 2;
+  p.ppu = 1;
+  const long long units = sel ? (long long)T / q_block + B : B;
+  long long items = units < T || !sel ? units : T;
+  if (p.rows) {
+    p.kind = sel ? paged::kUnits : paged::kWhole;
+  } else if (sel) {
+    p.kind = paged::kUnits;
+    p.ppu = (int)ceil_div64(rows, kPagedTileRows);
+    items *= p.ppu;
+  } else {
+    p.kind = paged::kRows;
+    items = (long long)T * G / kPagedTileRows + B;
+    const long long most = (long long)T * G;
+    items = items < most ? items : most;
+  }
+  p.items = (int)items;
+  p.min_split = 4;
+  const long long keys = (long long)max_pages * page;
+  const long long most = ceil_div64(ceil_div64(keys, p.rows ? kPagedRowsBN : kPagedTileBN), p.min_split);
+  // rows kernel: two CTAs per SM; one sequence fills one round of them, several (of unequal
+  // length) four, so that the last round is short.  tile kernel: one CTA per SM.
+  const long long want = p.rows ? (B == 1 ? 296 : 1184) : 148;
+  long long S = items * Hkv > 0 ? want / (items * Hkv) : 1;
+  S = S < most ? S : most;
+  S = S < 64 ? S : 64;
+  p.S = S < 1 ? 1 : (int)S;
+  return p;
+}
+
+cudaError_t launch_paged_rows(const paged::Args& a, const PagedPlan& pl, int d, int dtype, const void* kp,
+                              const void* vp, cudaStream_t st) {
+  CUtensorMap tk{}, tv{};
+  const unsigned long long rows = (unsigned long long)a.n_pages * a.Hkv * a.page;
+  const int box = a.page < kPagedRowsBN ? a.page : kPagedRowsBN;
+  cudaError_t e;
+  if ((e = make_tmap_bf16_rows(&tk, kp, rows, d, box)) != cudaSuccess) return e;
+  if ((e = make_tmap_bf16_rows(&tv, vp, rows, d, box)) != cudaSuccess) return e;
+  if (dtype == SPARSEPR_FP16) return d == 64 ? rows_d<__half, 64>(a, pl, tk, tv, st) : rows_d<__half, 128>(a, pl, tk, tv, st);
+  return d == 64 ? rows_d<__nv_bfloat16, 64>(a, pl, tk, tv, st) : rows_d<__nv_bfloat16, 128>(a, pl, tk, tv, st);
+}
+
+cudaError_t launch_paged_combine(const paged::Args& a, const PagedPlan& pl, int d, int dtype, cudaStream_t st) {
+  if (dtype == SPARSEPR_FP16) return d == 64 ? combine_t<__half, 64>(a, pl, st) : combine_t<__half, 128>(a, pl, st);
+  return d == 64 ? combine_t<__nv_bfloat16, 64>(a, pl, st) : combine_t<__nv_bfloat16, 128>(a, pl, st);
+}
+
+}  // namespace spr

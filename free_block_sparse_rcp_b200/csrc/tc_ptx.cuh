@@ -251,5 +251,12 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
   }
 }
 
+// After an abort: waits (at most kTimeoutNs) for a phase whose copies are in flight.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = gtimer();
+  while (!mbar_try(bar, parity) && gtimer() - t0 <= kTimeoutNs) {
+  }
+}
+
 }  // namespace tc
 }  // namespace spr

@@ -307,6 +307,176 @@ SPARSEPR_API int sparsepr_workspace_error(const sparsepr_params* p, void* worksp
 SPARSEPR_API sparsepr_status sparsepr_workspace_clear_error(const sparsepr_params* p, void* workspace,
                                                void* stream);
 
+/* ===========================================================================
+ * Rollouts frame by frame: rotary positions and a paged K/V cache
+ * ===========================================================================
+ * A rollout that generates its frames (or tokens) one after another keeps the keys and
+ * values of what it has generated in pages instead of calling sparsepr_forward on the
+ * whole sequence again: each step rotates its new queries and keys (sparsepr_rope, or
+ * inside sparsepr_cache_append), appends the keys and values to the pages, and attends
+ * from the new tokens to the cache (sparsepr_paged_attention), either to all of it or to
+ * the pages that a cheap score selects (sparsepr_page_select).
+ *
+ * The conventions at the top of this file hold (ownership, streams, argument errors,
+ * determinism), with these differences: tensors are bf16 or fp16 (rotary positions: fp32
+ * too), their rows are packed tokens with strides in the params, and the workspace is
+ * sparsepr_paged_workspace_bytes() with its own error query, sparsepr_paged_error().
+ * The entry points of this section never clear the error word except for
+ * sparsepr_paged_clear_error(): clear it once after allocating the workspace.  Calls that
+ * may overlap on the GPU need a workspace each.                                        */
+
+/* element types */
+#define SPARSEPR_BF16 0
+#define SPARSEPR_FP16 1
+#define SPARSEPR_FP32 2
+
+/* Rotary positions.  Pair i (0 <= i < rot_dim/2) of a row of token n turns by the angle
+ *   t = 2 pi * pos[axis(i)][n] * freq[i]                     (freq in turns per position)
+ *   y_a = m (x_a cos t - x_b sin t),  y_b = m (x_a sin t + x_b cos t)
+ * with (a, b) = (i, i + rot_dim/2) (layout 0, halves) or (2i, 2i + 1) (layout 1,
+ * interleaved); elements rot_dim .. d-1 are copied.  The pairs are divided into n_axes
+ * consecutive sections of axis_dim[a]/2 pairs (time, height, width of a video latent; one
+ * axis for text-like sequences).  Angles are reduced in 64 bits, so that positions up to
+ * 2^31 keep full accuracy.                                                             */
+typedef struct {
+  int B, H, N, d;          /* batch, heads, tokens (0 is allowed), head dim (2..512)                */
+  int H2;                  /* heads of the second tensor of the call (0: none)                      */
+  int dtype;               /* SPARSEPR_BF16, SPARSEPR_FP16 or SPARSEPR_FP32                         */
+  int rot_dim;             /* rotated elements of each row: even, 2..d                              */
+  int layout;              /* 0: halves, 1: interleaved                                             */
+  int n_axes;              /* position axes, 1..3                                                   */
+  int axis_dim[3];         /* rotated elements per axis: even, >= 2, summing to rot_dim             */
+  int pos_batched;         /* 0: pos is int32 [n_axes, N], 1: int32 [n_axes, B, N]                  */
+  int scaling;             /* of the frequencies theta^(-2j/axis_dim), j the pair within its axis:
+                              0 none; 1 linear: divided by factor;
+                              2 base: theta replaced by theta factor^(axis_dim/(axis_dim - 2));
+                              3 by parts: pairs that turn beta_fast times or more within orig_len
+                              positions keep their frequency, those that turn beta_slow times or
+                              less have it divided by factor, a linear ramp over j in between      */
+  int orig_len;            /* scaling 3: positions the frequencies were made for (>= 1)             */
+  double theta;            /* > 0 (10000)                                                           */
+  double factor;           /* > 0 (1)                                                               */
+  double beta_fast, beta_slow; /* scaling 3: beta_fast > beta_slow > 0 (32 and 1)                   */
+  double magnitude;        /* m; 0 means 1, or 0.1 ln(factor) + 1 with scaling 3                    */
+  long long x_stride[3], y_stride[3];    /* element strides of batch, head and token of the first
+                              tensor's input and output; all three 0 means contiguous [B,H,N,d].
+                              The last dimension is contiguous; an output stride may not be 0.     */
+  long long x2_stride[3], y2_stride[3];  /* the same for the second tensor                          */
+} sparsepr_rope_params;
+
+/* Fills freq[rot_dim/2] (HOST memory, turns per position) from the params; copy it to the
+ * device once and pass it to the calls below.  No CUDA call.                           */
+SPARSEPR_API sparsepr_status sparsepr_rope_frequencies(const sparsepr_rope_params* p, double* freq_host);
+
+/* Host-only validation of the params (no CUDA call). */
+SPARSEPR_API sparsepr_status sparsepr_rope_validate(const sparsepr_rope_params* p);
+
+/* y = rotation of x (and y2 of x2, with H2 heads, when H2 > 0), one launch for both.
+ * pos and freq (double [rot_dim/2]) are device pointers.  y may be x (in place) if their
+ * strides are equal; any other overlap is the caller's error.  No workspace.           */
+SPARSEPR_API sparsepr_status sparsepr_rope(const sparsepr_rope_params* p, const void* x, const int* pos,
+                                           const double* freq, void* y, const void* x2, void* y2, void* stream);
+
+/* Gradient of sparsepr_rope: dx = m R(-t) dy (x_stride describes dy, y_stride dx). */
+SPARSEPR_API sparsepr_status sparsepr_rope_backward(const sparsepr_rope_params* p, const void* dy, const int* pos,
+                                                    const double* freq, void* dx, const void* dy2, void* dx2,
+                                                    void* stream);
+
+/* A step of a rollout over B sequences with a paged K/V cache.
+ *   k_pages, v_pages  [n_pages, Hkv, page, d]  contiguous, 16-byte aligned
+ *   k_mean            [n_pages, Hkv, d]        mean key of each page's rows in use
+ *   page_table        int32 [B, max_pages]     page holding rows page*j .. page*j+page-1 of
+ *                                              sequence b (entries past its length are not read)
+ *   q_start           int32 [B+1]              first new token of each sequence among the T packed
+ *                                              rows (q_start[0] >= 0, nondecreasing, <= T; rows that
+ *                                              belong to no sequence are neither read nor written)
+ *   kv_len            int32 [B]                cached rows of each sequence, its new tokens included
+ * New token i of sequence b (n_b of them) has position kv_len[b] - n_b + i and row
+ * q_start[b] + i.  A negative position (n_b > kv_len[b]) is a token without a slot: it is not
+ * appended and, unless frame = 0, sees no key.                                          */
+typedef struct {
+  int B;                   /* sequences, 1..65536                                                   */
+  int Hq, Hkv;             /* query heads and key/value heads; Hkv divides Hq, query head h reads
+                              key/value head h / (Hq/Hkv)                                           */
+  int d;                   /* head dim, 64 or 128                                                   */
+  int dtype;               /* SPARSEPR_BF16 or SPARSEPR_FP16                                        */
+  int page;                /* rows per page: 16, 32, 64 or 128                                      */
+  int n_pages;             /* pages in the pool                                                     */
+  int max_pages;           /* row length of page_table (max_pages * page <= 2^30)                   */
+  int T;                   /* packed rows of new tokens (0 is allowed)                              */
+  int max_chunk;           /* no sequence of the call has more new tokens than this (>= 1); it picks
+                              the kernel, and a longer sequence is device error 1                   */
+  int frame;               /* mask: a token at position x sees the keys at positions y with
+                              floor(y/frame) <= floor(x/frame): 1 token-causal, the tokens of a frame
+                              for a frame-causal rollout; 0: every cached key                       */
+  float scale;             /* softmax scale; 0 means 1/sqrt(d)                                      */
+  int q_block;             /* selection: consecutive new tokens of a sequence that share a list    */
+  int n_select;            /* selection: pages of a list (0: no selection)                          */
+  int n_sink, n_recent;    /* selection: leading and trailing visible pages that every list holds
+                              (n_sink + n_recent <= n_select)                                       */
+  long long q_stride[2], o_stride[2]; /* element strides of token and head of Q and O; both 0 means
+                              contiguous [T, Hq, d].  Multiples of 8.                               */
+  long long k_stride[2], v_stride[2]; /* the same for the new K and V ([T, Hkv, d])                 */
+} sparsepr_cache_params;
+
+/* Host-only validation (no CUDA call), and the workspace of the calls below (0 if invalid). */
+SPARSEPR_API sparsepr_status sparsepr_cache_validate(const sparsepr_cache_params* p);
+SPARSEPR_API size_t sparsepr_paged_workspace_bytes(const sparsepr_cache_params* p);
+
+/* Writes the new K and V rows into their page slots and the mean key of every touched page
+ * (over its rows in use, taken of the stored keys in a fixed order, so that it does not
+ * depend on how the rows were split into calls).  With rope (NULL: none) the keys are
+ * rotated on the way: rope's rot_dim, layout, axes and magnitude count, pos is int32
+ * [n_axes, T] and rope_freq double [rot_dim/2] (both device); its other fields are not read
+ * except that d must agree.  Pages being written must belong to one sequence of the call.
+ * A page id out of [0, n_pages) is device error 1 and its rows are not written.         */
+SPARSEPR_API sparsepr_status sparsepr_cache_append(const sparsepr_cache_params* p, const void* K, const void* V,
+                                                   const int* q_start, const int* kv_len, const int* page_table,
+                                                   void* k_pages, void* v_pages, void* k_mean,
+                                                   const sparsepr_rope_params* rope, const int* pos,
+                                                   const double* rope_freq, void* workspace, size_t ws_bytes,
+                                                   void* stream);
+
+/* Lists of pages for sparsepr_paged_attention.  A unit is q_block consecutive new tokens of
+ * one sequence (the last one may be shorter); units are numbered sequence by sequence, and
+ * there are at most sparsepr_select_units(p) = T / q_block + B of them (min T).  For a unit
+ * and key/value head the score of a page is (mean of the unit's query rows over its tokens
+ * and the query heads of that key/value head) . k_mean[page], summed in 64 bits.  The pages
+ * that hold a key visible to the unit's last token take part; the first n_sink and the last
+ * n_recent of them are kept, and the best scores fill the list up to n_select (ties to the
+ * lowest page, NaN counts as the lowest score).
+ *   sel       int32 [units, Hkv, n_select]  page indices within the sequence, ascending, -1 behind
+ *   sel_count int32 [units, Hkv]            entries of each list
+ * Rows of units that do not exist are left as they were.  A page id out of [0, n_pages) is
+ * device error 1 and counts as the lowest score.                                        */
+SPARSEPR_API int sparsepr_select_units(const sparsepr_cache_params* p);
+SPARSEPR_API sparsepr_status sparsepr_page_select(const sparsepr_cache_params* p, const void* Q, const int* q_start,
+                                                  const int* kv_len, const int* page_table, const void* k_mean,
+                                                  int* sel, int* sel_count, void* workspace, size_t ws_bytes,
+                                                  void* stream);
+
+/* Attention of the new tokens over the cache:
+ *   O(i, h) = sum over visible keys j of softmax_j(s q.k_j) v_j,  lse(i, h) = ln sum exp(s q.k_j)
+ * (O [T, Hq, d]; lse float [T, Hq], may be NULL), over the pages of the token's list when sel
+ * and sel_count are given (n_select > 0), else over the whole cache.  A token that sees no
+ * key gets O = 0 and lse = -inf.  Keys past kv_len, and keys that no token of a block of
+ * rows sees, are never used, whatever their slots hold (a NaN or an infinity in a value row
+ * that some tokens of a block see can reach the block's other rows).
+ * A page id out of [0, n_pages), a list that is not strictly ascending or leaves the visible
+ * pages, or a kv_len out of [0, max_pages * page] is device error 1; the rows that depend on
+ * it become NaN.                                                                        */
+SPARSEPR_API sparsepr_status sparsepr_paged_attention(const sparsepr_cache_params* p, const void* Q,
+                                                      const int* q_start, const int* kv_len,
+                                                      const int* page_table, const void* k_pages,
+                                                      const void* v_pages, const int* sel, const int* sel_count,
+                                                      void* O, float* lse, void* workspace, size_t ws_bytes,
+                                                      void* stream);
+
+/* Error word of a paged workspace (0 = none; codes as above; -1 if it cannot be read) and
+ * its reset.  The query synchronizes `stream`; the reset only enqueues.                 */
+SPARSEPR_API int sparsepr_paged_error(const void* workspace, void* stream);
+SPARSEPR_API sparsepr_status sparsepr_paged_clear_error(void* workspace, void* stream);
+
 /* Human-readable status; sparsepr_last_error() gives the detail of the most recent
  * failing call on this host thread (static storage, never NULL).                      */
 SPARSEPR_API const char* sparsepr_status_string(sparsepr_status s);
