@@ -408,39 +408,67 @@ def run_call(p: Params, Q, K, V, ws=None, trace=False):
 # ---------------------------------------------------------------------------
 # Tensors may be strided views (the last dimension contiguous): their strides go into a copy
 # of the params, so one params object serves calls with different layouts.  Shapes, types and
-# devices are checked here, because the library sees pointers only.
-def _expect(name, t, shape, dtypes, device=None):
+# devices are checked here, because the library sees pointers only.  A step of a rollout makes
+# several of these calls, each shorter on the GPU than a few microseconds of Python, so the
+# checks compare first and build their messages only when something is wrong.
+_tc = None          # torch, and its types by code, from the first call on
+
+
+class _Torch:
+    def __init__(self):
+        import torch
+        self.mod = torch
+        self.elem = {BF16: torch.bfloat16, FP16: torch.float16, FP32: torch.float32}
+        self.i32, self.u8, self.f64, self.f32 = torch.int32, torch.uint8, torch.float64, torch.float32
+
+
+def _torch():
+    global _tc
+    if _tc is None:
+        _tc = _Torch()
+    return _tc
+
+
+def _expect(name, t, shape, dtype, dev):
+    """t has this shape and type and lies on device number dev (-1: the CPU)."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
+        return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if _type_name(t) not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(dtypes)}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _type_name(t):
-    return str(t.dtype).split(".")[-1]
-
-
-_NAMES = {BF16: "bfloat16", FP16: "float16", FP32: "float32"}
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} is on {t.device}, expected device {dev}")
 
 
 def _elem(p):
-    if p.dtype not in _NAMES:
+    dt = _torch().elem.get(p.dtype)
+    if dt is None:
         raise ValueError(f"unknown dtype code {p.dtype}")
-    return (_NAMES[p.dtype],)
+    return dt
 
 
-def _view(name, t, out, order):
-    """Element strides of the dimensions `order` of t into out; the rows must be contiguous."""
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    for i, d in enumerate(order):
-        # a dimension of one element has no stride of its own: take a contiguous one
-        out[i] = t.stride(d) if t.shape[d] > 1 else _packed(t, d)
-    if t.numel() and not any(out):     # all zero would mean contiguous to the library
-        raise ValueError(f"{name}: one row expanded over every dimension is not supported")
-    return ctypes.c_void_p(t.data_ptr())
+def _strided(p, first, views):
+    """p, or a copy of it with the element strides of each view's leading dimensions when one of
+    them is not contiguous.  views: (field, name, tensor or None); first: offset of the stride
+    fields, which make() leaves 0 (contiguous)."""
+    plain = not any(memoryview(p).cast("B")[first:])
+    if plain and all(t is None or t.is_contiguous() for _, _, t in views):
+        return p
+    q = type(p).from_buffer_copy(p)
+    for field, name, t in views:
+        out = getattr(q, field)
+        for i in range(len(out)):
+            out[i] = 0
+        if t is None or t.is_contiguous():
+            continue
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        for i in range(len(out)):
+            # a dimension of one element has no stride of its own: take a contiguous one
+            out[i] = t.stride(i) if t.shape[i] > 1 else _packed(t, i)
+        if t.numel() and not any(out):     # all zero would mean contiguous to the library
+            raise ValueError(f"{name}: one row expanded over every dimension is not supported")
+    return q
 
 
 def _packed(t, d):
@@ -450,12 +478,27 @@ def _packed(t, d):
     return n
 
 
-def _on(t):
-    """Launch on the tensor's device and its current stream."""
-    import torch
-    if t.device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
-    return torch.cuda.device(t.device)
+def _launch(fn, name, dev, *args):
+    """fn(*args, stream) on device dev and its current stream."""
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    torch = _torch().mod
+    stream = torch._C._cuda_getCurrentRawStream(dev)     # current_stream(dev).cuda_stream, without the object
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != 0:
+        raise SparsePRError(status, name)
+
+
+def _addr(t):
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return t.data_ptr()
 
 
 def sparsepr_rope_validate(p: RopeParams) -> int:
@@ -481,23 +524,23 @@ def rope_frequencies(p: RopeParams, device):
 
 
 def _rope(fn, name, p, x, pos, freq, y, x2, y2):
-    _check(_lib.sparsepr_rope_validate(ctypes.byref(p)), name)
-    q = RopeParams.from_buffer_copy(p)
+    _check(_lib.sparsepr_rope_validate(p), name)
     if (p.H2 > 0) != (x2 is not None) or (x2 is None) != (y2 is None):
         raise ValueError("the second tensor goes with H2 > 0")
-    dev, el = x.device, _elem(p)
-    ptrs = []
-    for nm, t, h, out in (("x", x, p.H, q.x_stride), ("y", y, p.H, q.y_stride), ("x2", x2, p.H2, q.x2_stride),
-                          ("y2", y2, p.H2, q.y2_stride)):
-        if t is None:
-            ptrs.append(None)
-            continue
-        _expect(nm, t, (p.B, h, p.N, p.d), el, dev)
-        ptrs.append(_view(nm, t, out, (0, 1, 2)))
-    _expect("pos", pos, (p.n_axes, p.B, p.N) if p.pos_batched else (p.n_axes, p.N), ("int32",), dev)
-    _expect("freq", freq, (p.rot_dim // 2,), ("float64",), dev)
-    with _on(x):
-        _check(fn(ctypes.byref(q), ptrs[0], _ptr(pos), _ptr(freq), ptrs[1], ptrs[2], ptrs[3], _stream(x)), name)
+    dev, el, B, N, d = x.get_device(), _elem(p), p.B, p.N, p.d
+    shape = (B, p.H, N, d)
+    _expect("x", x, shape, el, dev)
+    _expect("y", y, shape, el, dev)
+    if x2 is not None:
+        shape = (B, p.H2, N, d)
+        _expect("x2", x2, shape, el, dev)
+        _expect("y2", y2, shape, el, dev)
+    _expect("pos", pos, (p.n_axes, B, N) if p.pos_batched else (p.n_axes, N), _tc.i32, dev)
+    _expect("freq", freq, (p.rot_dim // 2,), _tc.f64, dev)
+    q = _strided(p, RopeParams.x_stride.offset, (("x_stride", "x", x), ("y_stride", "y", y), ("x2_stride", "x2", x2),
+                                                 ("y2_stride", "y2", y2)))
+    _launch(fn, name, dev, q, x.data_ptr(), _addr(pos), _addr(freq), y.data_ptr(),
+            None if x2 is None else x2.data_ptr(), None if y2 is None else y2.data_ptr())
 
 
 def sparsepr_rope(p: RopeParams, x, pos, freq, y, x2=None, y2=None):
@@ -527,13 +570,13 @@ def paged_workspace(p: CacheParams, device):
 
 
 def sparsepr_paged_error(ws) -> int:
-    with _on(ws):
+    torch = _torch().mod
+    with torch.cuda.device(ws.device):
         return _lib.sparsepr_paged_error(_ptr(ws), _stream(ws))
 
 
 def sparsepr_paged_clear_error(ws):
-    with _on(ws):
-        _check(_lib.sparsepr_paged_clear_error(_ptr(ws), _stream(ws)), "sparsepr_paged_clear_error")
+    _launch(_lib.sparsepr_paged_clear_error, "sparsepr_paged_clear_error", ws.get_device(), _addr(ws))
 
 
 def sparsepr_select_units(p: CacheParams) -> int:
@@ -564,81 +607,83 @@ def alloc_cache(p: CacheParams, device):
 
 
 def _sequences(p, dev, q_start, kv_len, page_table, ws):
-    i32 = ("int32",)
-    _expect("q_start", q_start, (p.B + 1,), i32, dev)
-    _expect("kv_len", kv_len, (p.B,), i32, dev)
-    _expect("page_table", page_table, (p.B, p.max_pages), i32, dev)
-    _expect("ws", ws, (ws.numel(),), ("uint8",), dev)
+    i32, B = _tc.i32, p.B
+    _expect("q_start", q_start, (B + 1,), i32, dev)
+    _expect("kv_len", kv_len, (B,), i32, dev)
+    _expect("page_table", page_table, (B, p.max_pages), i32, dev)
+    if ws.dtype is not _tc.u8 or ws.get_device() != dev:
+        raise ValueError("ws must be a uint8 tensor on the tensors' device")
 
 
-def _pages(p, dev, **tensors):
-    for nm, t in tensors.items():
-        _expect(nm, t, (p.n_pages, p.Hkv, p.d) if nm == "k_mean" else (p.n_pages, p.Hkv, p.page, p.d), _elem(p), dev)
+def _lists(p, dev, sel, sel_count):
+    n = _lib.sparsepr_select_units(p)
+    if n < 0:
+        sparsepr_select_units(p)     # raises
+    _expect("sel", sel, (n, p.Hkv, p.n_select), _tc.i32, dev)
+    _expect("sel_count", sel_count, (n, p.Hkv), _tc.i32, dev)
 
 
 def sparsepr_cache_append(p: CacheParams, K, V, q_start, kv_len, page_table, k_pages, v_pages, k_mean, ws, rope=None,
                           pos=None, freq=None):
     """Writes the new rows K, V [T, Hkv, d] into their page slots and the touched pages' mean
     keys; with rope (RopeParams) the keys are rotated by pos int32 [n_axes, T] on the way."""
-    _check(sparsepr_cache_validate(p), "sparsepr_cache_append")
-    q, dev, el = CacheParams.from_buffer_copy(p), K.device, _elem(p)
-    _expect("K", K, (p.T, p.Hkv, p.d), el, dev)
-    _expect("V", V, (p.T, p.Hkv, p.d), el, dev)
+    _check(_lib.sparsepr_cache_validate(p), "sparsepr_cache_append")
+    dev, el, T, Hkv, d = K.get_device(), _elem(p), p.T, p.Hkv, p.d
+    _expect("K", K, (T, Hkv, d), el, dev)
+    _expect("V", V, (T, Hkv, d), el, dev)
     _sequences(p, dev, q_start, kv_len, page_table, ws)
-    _pages(p, dev, k_pages=k_pages, v_pages=v_pages, k_mean=k_mean)
+    pages = (p.n_pages, Hkv, p.page, d)
+    _expect("k_pages", k_pages, pages, el, dev)
+    _expect("v_pages", v_pages, pages, el, dev)
+    _expect("k_mean", k_mean, (p.n_pages, Hkv, d), el, dev)
     if rope is not None:
         if pos is None or freq is None:
             raise ValueError("rope needs pos and freq")
-        _expect("pos", pos, (rope.n_axes, p.T), ("int32",), dev)
-        _expect("freq", freq, (rope.rot_dim // 2,), ("float64",), dev)
-    kp, vp = _view("K", K, q.k_stride, (0, 1)), _view("V", V, q.v_stride, (0, 1))
-    with _on(K):
-        _check(_lib.sparsepr_cache_append(ctypes.byref(q), kp, vp, _ptr(q_start), _ptr(kv_len), _ptr(page_table),
-                                          _ptr(k_pages), _ptr(v_pages), _ptr(k_mean),
-                                          None if rope is None else ctypes.byref(rope),
-                                          None if rope is None else _ptr(pos), None if rope is None else _ptr(freq),
-                                          _ptr(ws), ws.numel(), _stream(K)), "sparsepr_cache_append")
+        _expect("pos", pos, (rope.n_axes, T), _tc.i32, dev)
+        _expect("freq", freq, (rope.rot_dim // 2,), _tc.f64, dev)
+    else:
+        pos = freq = None
+    q = _strided(p, CacheParams.q_stride.offset, (("k_stride", "K", K), ("v_stride", "V", V)))
+    _launch(_lib.sparsepr_cache_append, "sparsepr_cache_append", dev, q, K.data_ptr(), V.data_ptr(), _addr(q_start),
+            _addr(kv_len), _addr(page_table), _addr(k_pages), _addr(v_pages), _addr(k_mean), rope, _addr(pos),
+            _addr(freq), _addr(ws), ws.numel())
 
 
 def sparsepr_page_select(p: CacheParams, Q, q_start, kv_len, page_table, k_mean, sel, sel_count, ws):
     """Page lists of every unit of q_block tokens and key/value head, by mean query . mean key."""
-    units = sparsepr_select_units(p)
-    q, dev = CacheParams.from_buffer_copy(p), Q.device
-    _expect("Q", Q, (p.T, p.Hq, p.d), _elem(p), dev)
+    _check(_lib.sparsepr_cache_validate(p), "sparsepr_page_select")
+    dev, el = Q.get_device(), _elem(p)
+    _expect("Q", Q, (p.T, p.Hq, p.d), el, dev)
     _sequences(p, dev, q_start, kv_len, page_table, ws)
-    _pages(p, dev, k_mean=k_mean)
-    _expect("sel", sel, (units, p.Hkv, p.n_select), ("int32",), dev)
-    _expect("sel_count", sel_count, (units, p.Hkv), ("int32",), dev)
-    qp = _view("Q", Q, q.q_stride, (0, 1))
-    with _on(Q):
-        _check(_lib.sparsepr_page_select(ctypes.byref(q), qp, _ptr(q_start), _ptr(kv_len), _ptr(page_table),
-                                         _ptr(k_mean), _ptr(sel), _ptr(sel_count), _ptr(ws), ws.numel(), _stream(Q)),
-               "sparsepr_page_select")
+    _expect("k_mean", k_mean, (p.n_pages, p.Hkv, p.d), el, dev)
+    _lists(p, dev, sel, sel_count)
+    q = _strided(p, CacheParams.q_stride.offset, (("q_stride", "Q", Q),))
+    _launch(_lib.sparsepr_page_select, "sparsepr_page_select", dev, q, Q.data_ptr(), _addr(q_start), _addr(kv_len),
+            _addr(page_table), _addr(k_mean), _addr(sel), _addr(sel_count), _addr(ws), ws.numel())
 
 
 def sparsepr_paged_attention(p: CacheParams, Q, q_start, kv_len, page_table, k_pages, v_pages, O, lse, ws, sel=None,
                              sel_count=None):
     """Attention of the new tokens Q [T, Hq, d] over the cache into O (and lse float32 [T, Hq] or
     None); with sel and sel_count over the pages of their lists."""
-    _check(sparsepr_cache_validate(p), "sparsepr_paged_attention")
-    q, dev, el = CacheParams.from_buffer_copy(p), Q.device, _elem(p)
-    _expect("Q", Q, (p.T, p.Hq, p.d), el, dev)
-    _expect("O", O, (p.T, p.Hq, p.d), el, dev)
+    _check(_lib.sparsepr_cache_validate(p), "sparsepr_paged_attention")
+    dev, el, T, Hq, d = Q.get_device(), _elem(p), p.T, p.Hq, p.d
+    _expect("Q", Q, (T, Hq, d), el, dev)
+    _expect("O", O, (T, Hq, d), el, dev)
     if lse is not None:
-        _expect("lse", lse, (p.T, p.Hq), ("float32",), dev)
+        _expect("lse", lse, (T, Hq), _tc.f32, dev)
     _sequences(p, dev, q_start, kv_len, page_table, ws)
-    _pages(p, dev, k_pages=k_pages, v_pages=v_pages)
+    pages = (p.n_pages, p.Hkv, p.page, d)
+    _expect("k_pages", k_pages, pages, el, dev)
+    _expect("v_pages", v_pages, pages, el, dev)
     if (sel is None) != (sel_count is None):
         raise ValueError("sel and sel_count come together")
     if sel is not None:
-        units = sparsepr_select_units(p)
-        _expect("sel", sel, (units, p.Hkv, p.n_select), ("int32",), dev)
-        _expect("sel_count", sel_count, (units, p.Hkv), ("int32",), dev)
-    qp, op = _view("Q", Q, q.q_stride, (0, 1)), _view("O", O, q.o_stride, (0, 1))
-    with _on(Q):
-        _check(_lib.sparsepr_paged_attention(ctypes.byref(q), qp, _ptr(q_start), _ptr(kv_len), _ptr(page_table),
-                                             _ptr(k_pages), _ptr(v_pages), _ptr(sel), _ptr(sel_count), op, _ptr(lse),
-                                             _ptr(ws), ws.numel(), _stream(Q)), "sparsepr_paged_attention")
+        _lists(p, dev, sel, sel_count)
+    q = _strided(p, CacheParams.q_stride.offset, (("q_stride", "Q", Q), ("o_stride", "O", O)))
+    _launch(_lib.sparsepr_paged_attention, "sparsepr_paged_attention", dev, q, Q.data_ptr(), _addr(q_start),
+            _addr(kv_len), _addr(page_table), _addr(k_pages), _addr(v_pages), _addr(sel), _addr(sel_count),
+            O.data_ptr(), _addr(lse), _addr(ws), ws.numel())
 
 
 def rollout_step(p: CacheParams, cache, Q, K, V, q_start, kv_len, page_table, O, ws, rope=None, pos=None, freq=None,
