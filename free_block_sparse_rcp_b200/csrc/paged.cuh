@@ -64,6 +64,19 @@ struct ProbShift<__half> {
   static constexpr float v = 7.f;
 };
 
+// Largest sum of a half chunk's probabilities against an earlier maximum: below fp16's largest
+// value; bf16 and the fp32 sums only need room below 2^128.
+template <typename T>
+struct ProbBound;
+template <>
+struct ProbBound<__nv_bfloat16> {
+  static constexpr float v = 18446744073709551616.f;   // 2^64
+};
+template <>
+struct ProbBound<__half> {
+  static constexpr float v = 32768.f;                  // 2^15
+};
+
 // ---------------------------------------------------------------------------
 // Arguments of the attention kernels
 // ---------------------------------------------------------------------------

@@ -510,7 +510,7 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int
     items *= p.ppu;
   } else {
     p.kind = paged::kRows;
-    items = (long long)T * G / kPagedTileRows + B;
+    items = ((long long)T * G + (kPagedTileRows - 1ll) * B) / kPagedTileRows;   // sum of ceil(n G / 256)
     const long long most = (long long)T * G;
     items = items < most ? items : most;
   }

@@ -31,10 +31,10 @@ using namespace spr::tc;
 constexpr int BM = 128, TPC = 2, BN = kPagedTileBN, KST = 3, VST = 2;
 constexpr int NSOFT = 256, PROD_WARP = 8, MMA_WARP = 9, NTT = 320;
 constexpr uint32_t kCols = 512;
-constexpr float kSpecSum = 256.0f;   // 2^8: largest row sum a speculative chunk may reach
 
 struct TileBars {
-  uint64_t q, kfull[KST], kempty[KST], vfull[VST], vempty[VST], vtail, s_full[TPC], p_full[TPC], o_done[TPC], mma_done;
+  uint64_t q, kfull[KST], kempty[KST], vfull[VST], vempty[VST], vtail, s_full[TPC], p_full[TPC][2], pv_half[TPC],
+      o_done[TPC], mma_done;
 };
 
 template <int D>
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(NTT, 1)
   constexpr float SHIFT = ProbShift<T>::v;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = su32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (base & 1023u) {
     if (tid == 0) set_error(a.err, DERR_INDEX);
     return;
@@ -139,7 +139,9 @@ __global__ void __launch_bounds__(NTT, 1)
     mbar_init(su32(&bars->vtail), 1);
     for (int t = 0; t < TPC; ++t) {
       mbar_init(su32(&bars->s_full[t]), 1);
-      mbar_init(su32(&bars->p_full[t]), 128);
+      mbar_init(su32(&bars->p_full[t][0]), 128);
+      mbar_init(su32(&bars->p_full[t][1]), 128);
+      mbar_init(su32(&bars->pv_half[t]), 1);
       mbar_init(su32(&bars->o_done[t]), 1);
     }
     mbar_init(su32(&bars->mma_done), 1);
@@ -234,63 +236,67 @@ __global__ void __launch_bounds__(NTT, 1)
     }
     __syncwarp();
   } else if (warp == MMA_WARP) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t IDS = idesc_t<T>(128, BN, false);
-      constexpr uint32_t IDO = idesc_t<T>(128, D, true);
-      bool ok = nch == 0 || wait(bars->q, 0);
-      auto count = [&](int t) -> int { return t == 0 ? nch0 : nch; };
-      auto first_user = [&](int j) -> int { return j < nch0 ? 0 : 1; };
-      // S_t = Q_t K_j^T; the last tile releases K_j
-      auto issue_s = [&](int t, int j) -> bool {
-        const int ks = j % KST;
-        if (t == first_user(j)) {
-          if (!wait(bars->kfull[ks], (j / KST) & 1)) return false;
-          tc_fence_after();
-        }
-        const uint32_t kb = sK + ks * L::kTile, qb = sQ + t * L::kTile;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-          tc_mma(tmem + 256 * t, sdesc(qb + off, 16, 1024), sdesc(kb + off, 16, 1024), IDS, k > 0 ? 1u : 0u);
-        }
-        tc_commit(su32(&bars->s_full[t]));
-        if (t == ntile - 1) tc_commit(su32(&bars->kempty[ks]));
-        return true;
-      };
-      // O_t += P_t V_j, P from TMEM; the last tile releases V_j
-      auto issue_pv = [&](int t, int j) -> bool {
-        const int vs = j % VST;
-        if (!wait(bars->p_full[t], j & 1)) return false;
-        if (t == first_user(j) && !wait(bars->vfull[vs], (j / VST) & 1)) return false;
+    // ---------------- MMA issuer (the whole warp, converged) ----------------
+    constexpr uint32_t IDS = idesc_t<T>(128, BN, false);
+    constexpr uint32_t IDO = idesc_t<T>(128, D, true);
+    const uint32_t lead = elect_one();
+    auto waits = [&](uint64_t& bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+    bool ok = nch == 0 || waits(bars->q, 0);
+    auto count = [&](int t) -> int { return t == 0 ? nch0 : nch; };
+    auto first_user = [&](int j) -> int { return j < nch0 ? 0 : 1; };
+    // S_t = Q_t K_j^T; the last tile releases K_j
+    auto issue_s = [&](int t, int j) -> bool {
+      const int ks = j % KST;
+      if (t == first_user(j)) {
+        if (!waits(bars->kfull[ks], (j / KST) & 1)) return false;
         tc_fence_after();
-        const uint32_t vb = sV + vs * L::kTile;
+      }
+      const uint64_t kd = sdesc(sK + ks * L::kTile, 16, 1024), qd = sdesc(sQ + t * L::kTile, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          tc_mma_ts(tmem + 256 * t + 128, tmem + 256 * t + k * 8, sdesc(vb + k * 2048, 16384, 1024), IDO,
-                    (j > 0 || k > 0) ? 1u : 0u);
-        if (t == ntile - 1) tc_commit(su32(&bars->vempty[vs]));
-        return true;
-      };
-      for (int t = 0; ok && t < ntile; ++t)
-        if (count(t) > 0) ok = issue_s(t, 0);
-      bool early0 = false;
-      for (int j = 0; ok && j < nch; ++j) {
-        for (int t = 0; ok && t < ntile; ++t) {
-          if (j >= count(t)) continue;
-          ok = issue_pv(t, j);
-          if (ok && j + 1 < count(t)) ok = issue_s(t, j + 1);
-          if (ok && t == 0 && ntile > 1 && j + 1 == nch0) {   // tile 0 may end before the item
-            tc_commit(su32(&bars->o_done[0]));
-            early0 = true;
-          }
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+        tc_mma_lead(lead, tmem + 256 * t, qd + off, kd + off, IDS, k > 0 ? 1u : 0u);
+      }
+      tc_commit_lead(lead, su32(&bars->s_full[t]));
+      if (t == ntile - 1) tc_commit_lead(lead, su32(&bars->kempty[ks]));
+      return true;
+    };
+    // O_t += P_t V_j, P from TMEM, half a chunk at a time; the last tile releases V_j
+    auto issue_pv = [&](int t, int j) -> bool {
+      const int vs = j % VST;
+      const uint64_t vd = sdesc(sV + vs * L::kTile, 16384, 1024);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        if (!waits(bars->p_full[t][hh], j & 1)) return false;
+        if (hh == 0 && t == first_user(j) && !waits(bars->vfull[vs], (j / VST) & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 4 * hh; k < 4 * hh + 4; ++k)
+          tc_mma_ts_lead(lead, tmem + 256 * t + 128, tmem + 256 * t + k * 8, vd + k * 128, IDO,
+                         (j > 0 || k > 0) ? 1u : 0u);
+        if (hh == 0) tc_commit_lead(lead, su32(&bars->pv_half[t]));
+      }
+      if (t == ntile - 1) tc_commit_lead(lead, su32(&bars->vempty[vs]));
+      return true;
+    };
+    for (int t = 0; ok && t < ntile; ++t)
+      if (count(t) > 0) ok = issue_s(t, 0);
+    bool early0 = false;
+    for (int j = 0; ok && j < nch; ++j) {
+      for (int t = 0; ok && t < ntile; ++t) {
+        if (j >= count(t)) continue;
+        ok = issue_pv(t, j);
+        if (ok && j + 1 < count(t)) ok = issue_s(t, j + 1);
+        if (ok && t == 0 && ntile > 1 && j + 1 == nch0) {   // tile 0 may end before the item
+          tc_commit_lead(lead, su32(&bars->o_done[0]));
+          early0 = true;
         }
       }
-      for (int t = 0; t < ntile; ++t)
-        if (!(t == 0 && early0)) tc_commit(su32(&bars->o_done[t]));
-      tc_commit(su32(&bars->mma_done));   // every MMA completes before the TMEM is released
-      if (!wait(bars->mma_done, 0)) drain_wait(su32(&bars->mma_done), 0);
     }
+    for (int t = 0; t < ntile; ++t)
+      if (!(t == 0 && early0)) tc_commit_lead(lead, su32(&bars->o_done[t]));
+    tc_commit_lead(lead, su32(&bars->mma_done));   // every MMA completes before the TMEM is released
+    if (!waits(bars->mma_done, 0) && lane == 0) drain_wait(su32(&bars->mma_done), 0);
     __syncwarp();
   } else {
     // ---------------- softmax + epilogue ----------------
@@ -317,96 +323,109 @@ __global__ void __launch_bounds__(NTT, 1)
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     if (t < ntile) {
-      uint32_t sreg[64];
-      uint32_t pk[64];
       const uint64_t sc2 = f2pack(a.scale_log2, a.scale_log2);
+      // 32 columns of S to probabilities against the running maximum; returns with the packed
+      // row sum in rs2
+      auto probs = [&](auto masked, const uint32_t* sr, uint32_t* pk, int left, uint64_t nmu2, uint64_t& rs2) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float s0 = __uint_as_float(sr[c]), s1 = __uint_as_float(sr[c + 1]);
+          if constexpr (decltype(masked)::value) {
+            if (c >= left) s0 = -INFINITY;
+            if (c + 1 >= left) s1 = -INFINITY;
+          }
+          float x0, x1;
+          f2unpack(ffma2(f2pack(s0, s1), sc2, nmu2), x0, x1);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          rs2 = fadd2(rs2, f2pack(p0, p1));
+          pk[c >> 1] = pack2<T>(p0, p1);
+        }
+      };
+      // half hh of chunk j against its own maximum: O is rescaled first
+      auto redo = [&](int j, int hh, int left, uint32_t* pk) {
+        uint32_t sr[32];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          tc_ld32(tS + 64 * hh + 32 * q, sr);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (32 * q + c < left) mx = fmaxf(mx, __uint_as_float(sr[c]));
+        }
+        const float m_new = fmaxf(m_used, mx * a.scale_log2);
+        float alpha = 1.f;
+        if (m_new > m_used) {
+          alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - m_new);
+          m_used = m_new;
+        }
+        // the products of the earlier chunks completed before S_t,j did; those of this chunk's
+        // first half are waited for
+        if (hh == 1) ok = ok && __all_sync(0xffffffffu, wait(bars->pv_half[t], j & 1));
+        if (j > 0 || hh == 1) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            tc_ld32(tO + c * 32, sr);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sr[e] = __float_as_uint(__uint_as_float(sr[e]) * alpha);
+            tc_st32(tO + c * 32, sr);
+          }
+        }
+        l *= alpha;
+        const float mu = (m_used == -INFINITY) ? 0.f : m_used - SHIFT;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          tc_ld32(tS + 64 * hh + 32 * q, sr);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float p0 = 32 * q + c < left ? ex2(__uint_as_float(sr[c]) * a.scale_log2 - mu) : 0.f;
+            const float p1 = 32 * q + c + 1 < left ? ex2(__uint_as_float(sr[c + 1]) * a.scale_log2 - mu) : 0.f;
+            l += p0 + p1;
+            pk[16 * q + (c >> 1)] = pack2<T>(p0, p1);
+          }
+        }
+      };
       for (int j = 0; j < nct; ++j) {
         ok = __all_sync(0xffffffffu, wait(bars->s_full[t], j & 1));
         if (!ok) break;
         tc_fence_after();
         const int valid = lim - (c0 + j) * BN;
         const bool full = __all_sync(0xffffffffu, valid >= BN);
-        bool need = true;
-        float mx = -INFINITY;
-        uint64_t rs2 = 0ull;
-        // one speculative pass against the running maximum, kept while the row sum stays small
-        const bool spec = __all_sync(0xffffffffu, m_used != -INFINITY);
-        if (spec) {
-          const float nm = SHIFT - m_used;
-          const uint64_t nmu2 = f2pack(nm, nm);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tc_ld32(tS + 32 * q, sreg);
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              float s0 = __uint_as_float(sreg[c]), s1 = __uint_as_float(sreg[c + 1]);
-              if (!full) {
-                if (32 * q + c >= valid) s0 = -INFINITY;
-                if (32 * q + c + 1 >= valid) s1 = -INFINITY;
-              }
-              float x0, x1;
-              f2unpack(ffma2(f2pack(s0, s1), sc2, nmu2), x0, x1);
-              const float p0 = ex2(x0), p1 = ex2(x1);
-              rs2 = fadd2(rs2, f2pack(p0, p1));
-              pk[16 * q + (c >> 1)] = pack2<T>(p0, p1);
-            }
-          }
-          float r0, r1;
-          f2unpack(rs2, r0, r1);
-          need = !(r0 + r1 <= kSpecSum * exp2f(SHIFT));
-        }
-        if (!__any_sync(0xffffffffu, need)) {
-          tc_st32(tS, pk);
-          tc_st32(tS + 32, pk + 32);
-          float r0, r1;
-          f2unpack(rs2, r0, r1);
-          l += r0 + r1;
-        } else {
-          // the chunk's own maximum, O rescaled, then P against it
+        uint32_t ra[32], rb[32], pk[32];
+        tc_ld32_start(tS, ra);
+        tc_ld32_start(tS + 32, rb);
+        tc_ld32_wait(ra);
+        tc_ld32_wait(rb);
+        // one speculative pass of each half against the running maximum, kept while the half's
+        // row sum stays in range
+        auto chunk = [&](auto masked) {
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            tc_ld64(tS + 64 * hh, sreg);
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (64 * hh + c < valid) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(sreg[c]));
-            mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-          }
-          const float m_new = fmaxf(m_used, mx * a.scale_log2);
-          float alpha = 1.f;
-          if (m_new > m_used) {
-            alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - m_new);
-            m_used = m_new;
-          }
-          if (j >= 1) {
-            // PV_t,j-1 completed before S_t,j did
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tc_ld32(tO + c * 32, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tc_st32(tO + c * 32, o);
+            const int left = valid - 64 * hh;
+            const bool spec = __all_sync(0xffffffffu, m_used != -INFINITY);
+            const float nm = SHIFT - m_used;
+            const uint64_t nmu2 = f2pack(nm, nm);
+            uint64_t rs2 = 0ull;
+            probs(masked, ra, pk, left, nmu2, rs2);
+            if (hh == 0) tc_ld32_start(tS + 64, ra);
+            probs(masked, rb, pk + 16, left - 32, nmu2, rs2);
+            if (hh == 0) tc_ld32_start(tS + 96, rb);
+            float r0, r1;
+            f2unpack(rs2, r0, r1);
+            const bool keep = spec && r0 + r1 <= ProbBound<T>::v;
+            if (hh == 0) {
+              tc_ld32_wait(ra);
+              tc_ld32_wait(rb);
             }
-          }
-          const float mu = (m_used == -INFINITY) ? 0.f : m_used - SHIFT;
-          float rs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            tc_ld64(tS + 64 * hh, sreg);
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              const float p0 = 64 * hh + c < valid ? ex2(__uint_as_float(sreg[c]) * a.scale_log2 - mu) : 0.f;
-              const float p1 = 64 * hh + c + 1 < valid ? ex2(__uint_as_float(sreg[c + 1]) * a.scale_log2 - mu) : 0.f;
-              rs[(c >> 1) & 3] += p0 + p1;
-              pk[c >> 1] = pack2<T>(p0, p1);
-            }
+            if (__all_sync(0xffffffffu, keep)) l += r0 + r1;
+            else redo(j, hh, left, pk);
             tc_st32(tS + 32 * hh, pk);
+            tc_fence_before();
+            mbar_arrive(su32(&bars->p_full[t][hh]));
           }
-          l = l * alpha + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
-        }
-        tc_fence_before();
-        mbar_arrive(su32(&bars->p_full[t]));
+        };
+        if (full) chunk(std::false_type{});
+        else chunk(std::true_type{});
       }
       if (ok && nct > 0) ok = __all_sync(0xffffffffu, wait(bars->o_done[t], 0));
       tc_fence_after();
