@@ -6,6 +6,12 @@
 #include "common.cuh"
 
 namespace spr {
+
+constexpr int kPagedTileRows = 256;   // query rows of an item of the tile kernel
+constexpr int kPagedRowsBN = 64;      // keys of a tile of the rows kernel
+constexpr int kPagedTileBN = 128;     // keys of a chunk of the tile kernel
+constexpr int kPlanCtas = 148;        // CTAs of the tile kernel
+
 namespace paged {
 
 // ---------------------------------------------------------------------------
@@ -89,8 +95,12 @@ struct Args {
   const int* sel_cnt;
   void* O;
   float* lse;
-  float* part_o;         // [S][T * Hq][d] of split units
-  float* part_lse;       // [S][T * Hq]
+  float* part_o;         // rows kernel [S][T * Hq][d], tile kernel [2 kPlanCtas][256][d]
+  float* part_lse;
+  void* plan;            // tile kernel: PlanHead
+  int* plan_seq;         // [B + 1] first item of each sequence
+  int* plan_item;        // [items] sequence of each item
+  long long* plan_pre;   // [items Hkv] inclusive prefix of the entries' chunks
   int* err;
   int B, Hq, Hkv, G, page, n_pages, max_pages, T, max_chunk, frame;
   int q_block, n_select;
@@ -282,8 +292,6 @@ cudaError_t launch_paged_rows(const paged::Args& a, const PagedPlan& pl, int d, 
 cudaError_t launch_paged_tiles(const paged::Args& a, const PagedPlan& pl, int d, int dtype, const void* kp,
                                const void* vp, cudaStream_t st);
 cudaError_t launch_paged_combine(const paged::Args& a, const PagedPlan& pl, int d, int dtype, cudaStream_t st);
-constexpr int kPagedTileRows = 256;   // query rows of an item of the tile kernel
-constexpr int kPagedRowsBN = 64;      // keys of a tile of the rows kernel
-constexpr int kPagedTileBN = 128;     // keys of a chunk of the tile kernel
+size_t tiles_plan_head_bytes();
 
 }  // namespace spr

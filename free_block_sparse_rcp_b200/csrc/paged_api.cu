@@ -210,20 +210,26 @@ int select_units(const sparsepr_cache_params& p) {
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Layout {
-  size_t part_lse, part_o, keys, total;
+  size_t part_lse, part_o, plan, plan_seq, plan_item, plan_pre, keys, total;
 };
 Layout layout_of(const sparsepr_cache_params& p) {
   Layout L{};
   size_t o = 256;   // error word
   auto take = [&](size_t bytes) { const size_t at = o; o = al256(o + bytes); return at; };
-  int S = plan_of(p, false).S;
-  if (p.n_select > 0) {
-    const int s = plan_of(p, true).S;
-    S = s > S ? s : S;
+  // partial results: rows of every split (rows kernel), or two pieces per CTA (tile kernel)
+  size_t rows = 0, items = 0;
+  for (int sel = 0; sel <= (p.n_select > 0 ? 1 : 0); ++sel) {
+    const PagedPlan pl = plan_of(p, sel != 0);
+    size_t r = pl.rows ? (pl.S > 1 ? (size_t)pl.S * p.T * p.Hq : 0) : 2ull * kPlanCtas * kPagedTileRows;
+    rows = r > rows ? r : rows;
+    if (!pl.rows && (size_t)pl.items > items) items = pl.items;
   }
-  const size_t rows = S > 1 ? (size_t)S * p.T * p.Hq : 0;
   L.part_lse = take(rows * 4);
   L.part_o = take(rows * p.d * 4);
+  L.plan = take(items ? tiles_plan_head_bytes() : 0);
+  L.plan_seq = take(items ? (p.B + 1ull) * 4 : 0);
+  L.plan_item = take(items * 4);
+  L.plan_pre = take(items * p.Hkv * 8);
   size_t keys = 0;
   if (p.n_select > 0) {
     const int units = select_units(p);
@@ -389,6 +395,10 @@ sparsepr_status sparsepr_paged_attention(const sparsepr_cache_params* p, const v
   a.O = O; a.lse = lse;
   a.part_lse = at<float>(workspace, L.part_lse);
   a.part_o = at<float>(workspace, L.part_o);
+  a.plan = at<char>(workspace, L.plan);
+  a.plan_seq = at<int>(workspace, L.plan_seq);
+  a.plan_item = at<int>(workspace, L.plan_item);
+  a.plan_pre = at<long long>(workspace, L.plan_pre);
   a.err = at<int>(workspace, 0);
   a.B = p->B; a.Hq = p->Hq; a.Hkv = p->Hkv; a.G = p->Hq / p->Hkv; a.page = p->page; a.n_pages = p->n_pages;
   a.max_pages = p->max_pages; a.T = p->T; a.max_chunk = p->max_chunk; a.frame = p->frame;
@@ -402,11 +412,11 @@ sparsepr_status sparsepr_paged_attention(const sparsepr_cache_params* p, const v
   cudaError_t e = pl.rows ? launch_paged_rows(a, pl, p->d, p->dtype, k_pages, v_pages, st)
                           : launch_paged_tiles(a, pl, p->d, p->dtype, k_pages, v_pages, st);
   if (e != cudaSuccess) return fail_cuda(e, "launch_paged_attention");
-  if (pl.S > 1) {
+  if (pl.rows && pl.S > 1) {
     e = launch_paged_combine(a, pl, p->d, p->dtype, st);
     if (e != cudaSuccess) return fail_cuda(e, "launch_paged_combine");
   }
-  set_launch_count(pl.S > 1 ? 2 : 1);
+  set_launch_count(!pl.rows ? 3 : (pl.S > 1 ? 2 : 1));
   return SPARSEPR_OK;
 }
 

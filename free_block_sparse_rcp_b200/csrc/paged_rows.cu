@@ -387,35 +387,16 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
 constexpr int kCombThreads = 256;
 
 template <typename T, int D, int KIND>
-__global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int rows_per_item, int bn) {
+__global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int max_rows) {
   __shared__ int s_find[kCombThreads / 32 + 2];
   const int idx = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Item it;
-  int row0 = 0, nrows;
-  if (KIND == kRows) {      // parts of whole sequences (tile kernel)
-    const int2 f = find_item<kRows, kCombThreads>(a.q_start, a.B, a.T, idx, a.G, rows_per_item, 1, 1, s_find);
-    if (f.x < 0) return;
-    it.s = load_seq(a, f.x);
-    it.tok0 = 0;
-    row0 = f.y * rows_per_item;
-    nrows = (int)min((long long)rows_per_item, (long long)it.s.n * a.G - row0);
-    const int last = (row0 + nrows - 1) / a.G;
-    it.total = visible_end(it.s.len - it.s.n + last, a.frame, it.s.len);
-  } else {
-    const int unit = idx / a.ppu, part = idx - unit * a.ppu;
-    if (!load_item<KIND, kCombThreads>(a, unit, h, s_find, it)) return;
-    row0 = part * rows_per_item;
-    nrows = min(rows_per_item, it.ntok * a.G - row0);
-    if (nrows <= 0) return;
-    if (a.ppu > 1 || KIND == kUnits) {
-      const int last = it.tok0 + (row0 + nrows - 1) / a.G;
-      it.total = stream_limit(visible_end(it.s.len - it.s.n + last, a.frame, it.s.len), it.list, it.cnt, a.page);
-    }
-  }
-  const int ns = split_count((it.total + bn - 1) / bn, a.S, a.min_split);
+  if (!load_item<KIND, kCombThreads>(a, idx, h, s_find, it)) return;
+  const int nrows = min(it.ntok * a.G, max_rows);
+  const int ns = split_count((it.total + BNR - 1) / BNR, a.S, a.min_split);
   if (ns <= 1) return;
   for (int r = warp; r < nrows; r += kCombThreads / 32) {
-    const int tok = (row0 + r) / a.G, qh = h * a.G + (row0 + r - tok * a.G);
+    const int tok = r / a.G, qh = h * a.G + (r - tok * a.G);
     const size_t qrow = (size_t)it.s.q0 + it.tok0 + tok, prow = qrow * a.Hq + qh, step = (size_t)a.T * a.Hq;
     float mx = -INFINITY;
     bool nan = false;
@@ -481,10 +462,9 @@ cudaError_t rows_d(const paged::Args& a, const PagedPlan& pl, const CUtensorMap&
 template <typename T, int D>
 cudaError_t combine_t(const paged::Args& a, const PagedPlan& pl, cudaStream_t st) {
   const dim3 grid(a.items, a.Hkv);
-  const int rows = pl.rows ? 16 * pl.mt : kPagedTileRows, bn = pl.rows ? kPagedRowsBN : kPagedTileBN;
-  if (pl.kind == paged::kUnits) paged::k_paged_combine<T, D, paged::kUnits><<<grid, paged::kCombThreads, 0, st>>>(a, rows, bn);
-  else if (pl.kind == paged::kRows) paged::k_paged_combine<T, D, paged::kRows><<<grid, paged::kCombThreads, 0, st>>>(a, rows, bn);
-  else paged::k_paged_combine<T, D, paged::kWhole><<<grid, paged::kCombThreads, 0, st>>>(a, rows, bn);
+  const int rows = 16 * pl.mt;
+  if (pl.kind == paged::kUnits) paged::k_paged_combine<T, D, paged::kUnits><<<grid, paged::kCombThreads, 0, st>>>(a, rows);
+  else paged::k_paged_combine<T, D, paged::kWhole><<<grid, paged::kCombThreads, 0, st>>>(a, rows);
   return cudaGetLastError();
 }
 
@@ -516,11 +496,12 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int
   }
   p.items = (int)items;
   p.min_split = 4;
-  const long long keys = (long long)max_pages * page;
-  const long long most = ceil_div64(ceil_div64(keys, p.rows ? kPagedRowsBN : kPagedTileBN), p.min_split);
-  // rows kernel: two CTAs per SM; one sequence fills one round of them, several (of unequal
-  // length) four, so that the last round is short.  tile kernel: one CTA per SM.
-  const long long want = p.rows ? (B == 1 ? 296 : 1184) : 148;
+  p.S = 1;
+  if (!p.rows) return p;
+  const long long most = ceil_div64(ceil_div64((long long)max_pages * page, kPagedRowsBN), p.min_split);
+  // two CTAs per SM; one sequence fills one round of them, several (of unequal length) four, so
+  // that the last round is short
+  const long long want = B == 1 ? 296 : 1184;
   long long S = items * Hkv > 0 ? want / (items * Hkv) : 1;
   S = S < most ? S : most;
   S = S < 64 ? S : 64;
