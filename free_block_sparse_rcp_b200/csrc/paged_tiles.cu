@@ -69,6 +69,10 @@ struct TileLayout {
 };
 static_assert(sizeof(TileBars) <= 256 && 2 * sizeof(Seg) <= 256, "barrier and segment blocks");
 
+// Taking up an entry (its rows, the first softmax, the epilogue) costs about as much as two chunks:
+// an entry's cost begins with that many.
+constexpr int kEntryCost = 2;
+
 // ---------------------------------------------------------------------------
 // The plan (one block).  Entries e = h n_items + r, item n_items - 1 - r: the last parts of a
 // causal sequence see the most keys and come first.
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_tiles_plan(Args a) {
       const int c = min(max(a.sel_cnt[(size_t)(item / a.ppu) * a.Hkv + h], 0), a.n_select);
       keys = min(c * a.page, keys);
     }
-    return max(1, (keys + BN - 1) / BN);
+    return kEntryCost + (keys + BN - 1) / BN;
   };
   long long mine = 0, W;
   int mx = 0;
@@ -229,7 +233,7 @@ __device__ __forceinline__ long long find_entry(const long long* __restrict__ pr
   return lo;
 }
 
-// Entry e, chunks [x0, x1) of its `cost`.
+// Entry e, [x0, x1) of its `cost`.
 template <bool SEL>
 __device__ __forceinline__ void make_seg(const Args& a, long long e, int n_items, int x0, int x1, int cost, int cta, Seg& g) {
   g.h = (int)(e / n_items);
@@ -259,8 +263,8 @@ __device__ __forceinline__ void make_seg(const Args& a, long long e, int n_items
   g.total = limit_of(g.nrows - 1);
   const int chunks = (g.total + BN - 1) / BN;
   g.slot = x0 == 0 && x1 == cost ? -1 : (x0 > 0 ? 2 * cta : 2 * cta + 1);
-  g.c0 = min(x0, chunks);
-  g.nch = min(x1, chunks) - g.c0;
+  g.c0 = min(max(x0 - kEntryCost, 0), chunks);
+  g.nch = min(max(x1 - kEntryCost, 0), chunks) - g.c0;
   // tile 0 stops at its own last row's limit
   g.nch0 = g.nrows <= BM ? g.nch : min(g.nch, max(0, (limit_of(BM - 1) + BN - 1) / BN - g.c0));
 }
