@@ -229,16 +229,27 @@ __global__ void __launch_bounds__(kSelThreads) k_page_score(SelectArgs a) {
     const int c = tid % CH, g0 = tid / CH;
     double s[8] = {0., 0., 0., 0., 0., 0., 0., 0.};
     bool bad = false;
-    for (int r = g0; r < u.ntok * G; r += RG) {
-      const int t = r / G, gh = r - t * G;
-      const uint4 w = *reinterpret_cast<const uint4*>((const T*)a.Q + (u.tok0 + t) * a.qst +
-                                                      (long long)(h * G + gh) * a.qsh + c * 8);
-      const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+    const int rows = u.ntok * G;
+    constexpr int UQ = 8;               // rows in flight
+    for (int r = g0; r < rows; r += UQ * RG) {
+      uint4 w[UQ];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bad |= not_finite<T>(p[i]);
-        s[2 * i] += wide<T>(p[i]);
-        s[2 * i + 1] += wide<T>(p[i] >> 16);
+      for (int k = 0; k < UQ; ++k) {
+        const int rr = r + k * RG;
+        w[k] = make_uint4(0, 0, 0, 0);
+        if (rr >= rows) continue;
+        const int t = rr / G, gh = rr - t * G;
+        w[k] = *reinterpret_cast<const uint4*>((const T*)a.Q + (u.tok0 + t) * a.qst + (long long)(h * G + gh) * a.qsh + c * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < UQ; ++k) {
+        const uint32_t p[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bad |= not_finite<T>(p[i]);
+          s[2 * i] += wide<T>(p[i]);
+          s[2 * i + 1] += wide<T>(p[i] >> 16);
+        }
       }
     }
     // a NaN or an infinity in a query row: every score of the unit is NaN
@@ -264,46 +275,66 @@ __global__ void __launch_bounds__(kSelThreads) k_page_score(SelectArgs a) {
 #pragma unroll
   for (int i = 0; i < CPL; ++i) q[i] = s_q[(i / 8) * 64 + sub * 8 + (i & 7)];
   const int p0 = (int)((long long)u.vis * split / a.splits), p1 = (int)((long long)u.vis * (split + 1) / a.splits);
-  constexpr int PPB = kSelThreads / 8, UN = 2;   // pages of the block per step, steps in flight
+  constexpr int PPB = kSelThreads / 8, UN = 4;   // pages of the block per step, steps in flight
   const int* table = a.table + (size_t)u.b * a.max_pages;
-  for (int j0 = p0; j0 < p1; j0 += PPB * UN) {
-    uint4 w[UN][CPL / 8];
-    bool ok[UN];
+  // ids are loaded two rounds ahead of their scores, means one round
+  auto ids = [&](int j0, int* id) {
 #pragma unroll
     for (int s = 0; s < UN; ++s) {
       const int j = j0 + s * PPB + (tid >> 3);
-      ok[s] = false;
-      if (j < p1) {
-        const int pid = table[j];
-        ok[s] = pid >= 0 && pid < a.n_pages;
-        if (!ok[s] && sub == 0) set_error(a.err, DERR_INDEX);
-        const T* row = (const T*)a.km + ((size_t)(ok[s] ? pid : 0) * a.Hkv + h) * D;
-#pragma unroll
-        for (int c = 0; c < CPL / 8; ++c) w[s][c] = *reinterpret_cast<const uint4*>(row + c * 64 + sub * 8);
-      } else {
-#pragma unroll
-        for (int c = 0; c < CPL / 8; ++c) w[s][c] = make_uint4(0, 0, 0, 0);
-      }
+      id[s] = j < p1 ? table[j] : -2;
     }
+  };
+  auto means = [&](const int* id, uint4 (*w)[CPL / 8]) {
+#pragma unroll
+    for (int s = 0; s < UN; ++s) {
+      if (id[s] < 0 || id[s] >= a.n_pages) continue;
+      const T* row = (const T*)a.km + ((size_t)id[s] * a.Hkv + h) * D;
+#pragma unroll
+      for (int c = 0; c < CPL / 8; ++c) w[s][c] = *reinterpret_cast<const uint4*>(row + c * 64 + sub * 8);
+    }
+  };
+  int id0[UN], id1[UN];
+  uint4 w[UN][CPL / 8];
+  ids(p0, id0);
+  ids(p0 + PPB * UN, id1);
+  means(id0, w);
+  for (int j0 = p0; j0 < p1; j0 += PPB * UN) {
+    int id2[UN];
+    uint4 wn[UN][CPL / 8];
+    ids(j0 + 2 * PPB * UN, id2);
+    means(id1, wn);
 #pragma unroll
     for (int s = 0; s < UN; ++s) {
       const int j = j0 + s * PPB + (tid >> 3);
+      const bool ok = id0[s] >= 0 && id0[s] < a.n_pages;
       double x = 0.;
-      bool bad = false;
+      bool bad = !ok;
+      if (ok) {
 #pragma unroll
-      for (int c = 0; c < CPL / 8; ++c) {
-        const uint32_t p[4] = {w[s][c].x, w[s][c].y, w[s][c].z, w[s][c].w};
+        for (int c = 0; c < CPL / 8; ++c) {
+          const uint32_t p[4] = {w[s][c].x, w[s][c].y, w[s][c].z, w[s][c].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          bad |= not_finite<T>(p[i]);
-          x = fma(wide<T>(p[i]), q[c * 8 + 2 * i], x);
-          x = fma(wide<T>(p[i] >> 16), q[c * 8 + 2 * i + 1], x);
+          for (int i = 0; i < 4; ++i) {
+            bad |= not_finite<T>(p[i]);
+            x = fma(wide<T>(p[i]), q[c * 8 + 2 * i], x);
+            x = fma(wide<T>(p[i] >> 16), q[c * 8 + 2 * i + 1], x);
+          }
         }
+      } else if (id0[s] != -2 && sub == 0) {
+        set_error(a.err, DERR_INDEX);
       }
-      if (bad || !ok[s]) x = __longlong_as_double(0x7ff8000000000000ll);
+      if (bad) x = __longlong_as_double(0x7ff8000000000000ll);
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
       if (j < p1 && sub == 0) keys[j] = order_key(x);
+    }
+#pragma unroll
+    for (int s = 0; s < UN; ++s) {
+      id0[s] = id1[s];
+      id1[s] = id2[s];
+#pragma unroll
+      for (int c = 0; c < CPL / 8; ++c) w[s][c] = wn[s][c];
     }
   }
   if (a.splits > 1) return;

@@ -249,7 +249,7 @@ struct AppendArgs {
   const int* pos;                 // NULL: no rotation
   const double* freq;
   int* err;
-  int B, Hkv, d, dtype, page, n_pages, max_pages, T;
+  int B, Hkv, d, dtype, page, n_pages, max_pages, T, max_chunk;
   int rot, layout, n_axes, axis_pairs[3];
   float mag;
   long long kst, ksh, vst, vsh;

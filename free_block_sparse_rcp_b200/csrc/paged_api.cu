@@ -330,12 +330,12 @@ sparsepr_status sparsepr_cache_append(const sparsepr_cache_params* p, const void
   a.kp = k_pages; a.vp = v_pages; a.km = k_mean;
   a.err = at<int>(workspace, 0);
   a.B = p->B; a.Hkv = p->Hkv; a.d = p->d; a.dtype = p->dtype; a.page = p->page; a.n_pages = p->n_pages;
-  a.max_pages = p->max_pages; a.T = p->T;
+  a.max_pages = p->max_pages; a.T = p->T; a.max_chunk = p->max_chunk;
   strides2(p->k_stride, p->Hkv, p->d, a.kst, a.ksh);
   strides2(p->v_stride, p->Hkv, p->d, a.vst, a.vsh);
   const cudaError_t e = launch_cache_append(a, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "launch_cache_append");
-  set_launch_count(1);
+  set_launch_count(2);
   return SPARSEPR_OK;
 }
 

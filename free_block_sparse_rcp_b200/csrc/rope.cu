@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
       }
       continue;
     }
-    constexpr int UN = MODE == kInter ? 4 : 2;   // heads in flight
+    constexpr int UN = 4;   // heads in flight
     int h = first;
     for (; h + (UN - 1) * gy < a.H[t]; h += UN * gy) {
       uint4 wa[UN], wb[UN];
@@ -219,9 +219,10 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
   const long long units = (long long)a.B * a.N * RowUnits<T, MODE>::count(a.d, a.rot);
   const long long blocks = ceil_div64(units, kRopeThreads);
   const int heads = a.H[0] + a.H[1];
-  // Heads are dealt to enough blocks for eight rounds of the GPU's resident blocks (148 SMs x
-  // 8): few tokens get one head per block, and many tokens a last round that is a small share.
-  long long hs = ceil_div64(8 * 148 * 8, blocks);
+  // Heads are dealt to enough blocks for six rounds of four resident blocks per SM: few tokens get
+  // one head per block, and many tokens a last round that is a small share, while the angles
+  // still serve several heads.
+  long long hs = ceil_div64(6 * 148 * 4, blocks);
   hs = hs < heads ? hs : heads;
   k_rope<T, MODE><<<dim3((unsigned)blocks, (unsigned)hs), kRopeThreads, 0, st>>>(a, units);
   return cudaGetLastError();
@@ -238,94 +239,42 @@ cudaError_t launch_rope_m(const RopeArgs& a, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // Cache append
 // ---------------------------------------------------------------------------
-// grid (page slots that the call can touch, head groups), one block = one touched page of one
-// sequence and hpb heads: new rows of K (rotated) and V go to their slots, and the page's mean
-// key is taken over all its rows in use.  The sum over rows has a fixed order (row r belongs
-// to row group r mod RG, the groups are added in order), so the mean depends on the page's
-// contents alone.
-constexpr int kAppThreads = 256;
+// Two kernels.  k_cache_rows moves the new rows of K (rotated) and V to their slots, a thread per
+// unit of a token as in k_rope, so that a token's angles serve its heads from registers.
+// k_page_means then takes the mean key of every touched page over its rows in use; the page's
+// new rows come from L2.  Its sum over rows has a fixed order (row r belongs to row group
+// r mod RG, the groups are added in order), so the mean depends on the page's contents alone.
+// Both together in one block per page had to hold a page's angles in shared memory and its blocks
+// waited for one another's latencies: 38 us for 4 x 1,024 tokens of 16 heads (d 128) on pages of
+// 128, against the 10 us that the 67 MB need.
+
+// Sequence that holds packed row t (-1: none), by the whole warp: 32 probes a step.
+__device__ __forceinline__ int find_seq(const int* __restrict__ q_start, int B, int t, int lane) {
+  int lo = 0, n = B;            // the last b in [lo, lo + n) with q_start[b] <= t
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int i = lane * step;
+    const bool le = i < n && q_start[lo + i] <= t;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, le));
+    const int at = cnt > 0 ? (cnt - 1) * step : 0;
+    lo += at;
+    n = min(step, n - at);
+  }
+  return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
+}
 
 template <typename T, int MODE, bool ROPE>
-__global__ void __launch_bounds__(kAppThreads) k_cache_append(AppendArgs a, int hpb) {
+__global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
   using U = RowUnits<T, MODE>;
-  constexpr int E = U::E, P = U::P;
-  constexpr int NC = MODE == kHalf ? 2 * E : (MODE == kInter ? E : 2);   // columns of a unit
-  extern __shared__ __align__(16) unsigned char sm_app[];
-  __shared__ int sm_find[kAppThreads / 32 + 4];
-  const int tid = threadIdx.x;
+  constexpr int E = U::E, P = U::P, UN = 2;   // heads of a batch; one batch is loaded ahead
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int lane = threadIdx.x & 31;
   const int d = a.d, page = a.page, rot = ROPE ? a.rot : 0, half = rot / 2;
-  // sequence b and its touched page: pages floor((len - n) / page) .. floor((len - 1) / page)
-  const int2 it = [&]() {
-    const int lane = tid & 31, warp = tid >> 5;
-    const int run = (a.B + kAppThreads - 1) / kAppThreads;
-    const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
-    auto count = [&](int b) -> int {
-      const int lo = min(max(a.q_start[b], 0), a.T);
-      const int n = max(0, min(a.q_start[b + 1], a.T) - lo);
-      const int len = min(max(a.kv_len[b], 0), a.max_pages * page);
-      if (n == 0 || len == 0) return 0;
-      return (len - 1) / page - max(len - n, 0) / page + 1;
-    };
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += count(b);
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) sm_find[warp] = inc;
-    if (tid == 0) sm_find[kAppThreads / 32] = -1;
-    __syncthreads();
-    int at = inc - mine;
-    for (int w = 0; w < warp; ++w) at += sm_find[w];
-    const int idx = blockIdx.x;
-    if (idx >= at && idx < at + mine) {
-      for (int b = b0; b < b1; ++b) {
-        const int c = count(b);
-        if (idx < at + c) {
-          sm_find[kAppThreads / 32] = b;
-          sm_find[kAppThreads / 32 + 1] = idx - at;
-          break;
-        }
-        at += c;
-      }
-    }
-    __syncthreads();
-    return make_int2(sm_find[kAppThreads / 32], sm_find[kAppThreads / 32 + 1]);
-  }();
-  if (it.x < 0) return;
-  const int b = it.x;
-  const int qs = a.q_start[b], qe = a.q_start[b + 1], lenr = a.kv_len[b];
-  const int q0 = min(max(qs, 0), a.T), n = max(0, min(qe, a.T) - q0);
-  const int len = min(max(lenr, 0), a.max_pages * page);
-  if (tid == 0 && blockIdx.y == 0 && (qs < 0 || qe > a.T || len != lenr)) set_error(a.err, DERR_INDEX);
-  const int s0 = max(len - n, 0);                 // first new slot
-  const int j = s0 / page + it.y;                 // page of the sequence
-  const int pid = a.table[(size_t)b * a.max_pages + j];
-  if (pid < 0 || pid >= a.n_pages) {
-    if (tid == 0) set_error(a.err, DERR_INDEX);
-    return;
-  }
-  const int base = j * page;
-  const int r0 = max(s0, base) - base, r1 = min(len, base + page) - base;   // new rows of the page
-  const int tok = q0 + (base + r0) - (len - n);    // packed row of page row r0
-  // cos and sin of every (new row, pair)
-  float2* tab = reinterpret_cast<float2*>(sm_app);
-  if (ROPE) {
-    const Axes ax{a.n_axes, {a.axis_pairs[0], a.axis_pairs[1], a.axis_pairs[2]}};
-    for (int e = tid; e < (r1 - r0) * half; e += kAppThreads) {
-      const int r = e / half, p = e - r * half;
-      const float2 cs = turn<false>((double)a.pos[(size_t)ax.of(p) * a.T + tok + r] * a.freq[p]);
-      tab[e] = make_float2(cs.x * a.mag, cs.y * a.mag);
-    }
-    __syncthreads();
-  }
   const int upr = U::count(d, rot);
-  const int RG = kAppThreads / upr;                // rows in flight
-  const int rg = tid / upr, u = tid - rg * upr;
-  const bool on = rg < RG;
-  int e0, e1 = 0, p0 = 0;
+  const long long gid = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
+  const int row = (int)min(gid / upr, (long long)a.T);       // a.T: past the last row
+  const int u = (int)(gid - (long long)row * upr);
+  int e0, e1 = 0, p0;
   bool turns = false;
   if (MODE == kInter) {
     e0 = u * E;
@@ -342,123 +291,258 @@ __global__ void __launch_bounds__(kAppThreads) k_cache_append(AppendArgs a, int 
     e0 = !turns ? rot + (u - half) : (a.layout == 0 ? u : 2 * u);
     e1 = a.layout == 0 ? e0 + half : e0 + 1;
   }
-  float* red = reinterpret_cast<float*>(sm_app + (ROPE ? (size_t)page * half * 8 : 0));   // [RG][d]
-  for (int h = blockIdx.y * hpb; h < min(a.Hkv, (int)(blockIdx.y + 1) * hpb); ++h) {
-    T* kp = (T*)a.kp + ((size_t)pid * a.Hkv + h) * page * d;
-    T* vp = (T*)a.vp + ((size_t)pid * a.Hkv + h) * page * d;
-    const T* K = (const T*)a.K + tok * a.kst + h * a.ksh;
-    const T* V = (const T*)a.V + tok * a.vst + h * a.vsh;
-    float acc[NC];
+  // value chunks of the unit: u and u + upr, as far as the row has them (upr is at least half of
+  // its chunks)
+  constexpr int VE = Vec<T>::E;
+  const int f0 = u * VE < d ? u * VE : -1, f1 = (u + upr) * VE < d ? (u + upr) * VE : -1;
+  const bool live = row < a.T;
+  const T* K = (const T*)a.K + (live ? row * a.kst : 0);
+  const T* V = (const T*)a.V + (live ? row * a.vst : 0);
+  const int gy = gridDim.y;
+  struct Batch {
+    uint4 ka[UN], kb[UN], va[UN], vb[UN];
+  };
+  auto load = [&](Batch& w, int h0) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) acc[i] = 0.f;
-    if (on) {
-      for (int r = rg; r < r1; r += RG) {
-        const bool fresh = r >= r0;
-        const T* src = fresh ? K + (r - r0) * a.kst : kp + (size_t)r * d;
-        const float2* cs = tab + (size_t)(r - r0) * half + p0;
-        if (MODE == kPair) {
-          float va = as_f32(src[e0]), vb = turns ? as_f32(src[e1]) : 0.f;
-          if (fresh) {
-            if (turns) {
-              const float2 t = *cs;
-              const float p = va, q = vb;
-              va = as_f32(from_f32<T>(p * t.x - q * t.y));
-              vb = as_f32(from_f32<T>(p * t.y + q * t.x));
-              kp[(size_t)r * d + e1] = from_f32<T>(vb);
-            }
-            kp[(size_t)r * d + e0] = from_f32<T>(va);
-          }
-          acc[0] += va;
-          acc[1] += vb;
-        } else {
-          uint4 wa, wb = make_uint4(0, 0, 0, 0);
-          float va[E], vb[E];
-          Vec<T>::load(src + e0, wa);
-          if (MODE == kHalf && turns) Vec<T>::load(src + e1, wb);
-          Vec<T>::unpack(wa, va);
-          Vec<T>::unpack(wb, vb);
-          if (fresh) {
-            if (turns) {
-              if (MODE == kInter) {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                  const float2 t = p0 + i < half ? cs[i] : make_float2(1.f, 0.f);
-                  const float p = va[2 * i], q = va[2 * i + 1];
-                  va[2 * i] = p * t.x - q * t.y;
-                  va[2 * i + 1] = p * t.y + q * t.x;
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                  const float2 t = cs[i];
-                  const float p = va[i], q = vb[i];
-                  va[i] = p * t.x - q * t.y;
-                  vb[i] = p * t.y + q * t.x;
-                }
-                wb = Vec<T>::pack(vb);
-                Vec<T>::unpack(wb, vb);
-                *reinterpret_cast<uint4*>(kp + (size_t)r * d + e1) = wb;
-              }
-              wa = Vec<T>::pack(va);
-              Vec<T>::unpack(wa, va);   // the mean is of the stored keys
-            }
-            *reinterpret_cast<uint4*>(kp + (size_t)r * d + e0) = wa;
-          }
-#pragma unroll
-          for (int i = 0; i < E; ++i) acc[i] += va[i];
-          if (MODE == kHalf) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) acc[E + i] += vb[i];
-          }
+    for (int i = 0; i < UN; ++i) {
+      const int h = h0 + i * gy;
+      if (!live || h >= a.Hkv) continue;
+      if (MODE != kPair) Vec<T>::load(K + h * a.ksh + e0, w.ka[i]);
+      if (MODE == kHalf && turns) Vec<T>::load(K + h * a.ksh + e1, w.kb[i]);
+      if (f0 >= 0) Vec<T>::load(V + h * a.vsh + f0, w.va[i]);
+      if (f1 >= 0) Vec<T>::load(V + h * a.vsh + f1, w.vb[i]);
+    }
+  };
+  Batch cur;
+  load(cur, blockIdx.y);       // in flight while the slot and the angles are found
+  // the sequences of the warp's rows: one search, then steps
+  int b = -1;
+  {
+    const int first = __shfl_sync(0xffffffffu, row, 0), last = min(__shfl_sync(0xffffffffu, row, 31), a.T - 1);
+    if (first < a.T) {
+      b = find_seq(a.q_start, a.B, first, lane);
+      if (b >= 0 && a.q_start[b + 1] <= last)        // the warp's rows leave the first one's sequence
+        while (b < a.B && row >= a.q_start[b + 1]) ++b;
+      if (b < 0)                                     // rows that belong to no sequence, or broken offsets
+        for (int r = first; r <= last; ++r) {
+          const int f = find_seq(a.q_start, a.B, r, lane);
+          if (r == row) b = f;
         }
-      }
-      // column sums of this row group
-      float* row = red + (size_t)rg * d;
-      if (MODE == kPair) {
-        row[e0] = acc[0];
-        if (turns) row[e1] = acc[1];
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) row[e0 + i] = acc[i];
-        if (MODE == kHalf && turns) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) row[e1 + i] = acc[E + i];
-        }
-      }
     }
-    // V rows
-    const int cpr = d / E;
-    for (int e = tid; e < (r1 - r0) * cpr; e += kAppThreads) {
-      const int r = e / cpr, c = e - r * cpr;
-      *reinterpret_cast<uint4*>(vp + (size_t)(r0 + r) * d + c * E) =
-          *reinterpret_cast<const uint4*>(V + r * a.vst + c * E);
-    }
-    __syncthreads();
-    if (tid < d) {
-      float s = 0.f;
-      for (int g = 0; g < RG; ++g) s += red[(size_t)g * d + tid];
-      ((T*)a.km)[((size_t)pid * a.Hkv + h) * d + tid] = from_f32<T>(s / (float)r1);
-    }
-    __syncthreads();
   }
+  if (!live || b < 0 || b >= a.B || row < a.q_start[b]) return;
+  const int qs = a.q_start[b], qe = a.q_start[b + 1], lenr = a.kv_len[b];
+  const int n = qe - qs, len = min(max(lenr, 0), a.max_pages * page);
+  if (u == 0 && row == qs && blockIdx.y == 0 && (qs < 0 || qe > a.T || len != lenr || n > a.max_chunk))
+    set_error(a.err, DERR_INDEX);
+  const int slot = len - n + (row - qs);
+  if (slot < 0 || slot >= len) return;
+  const int j = slot / page;
+  const int pid = a.table[(size_t)b * a.max_pages + j];
+  if (pid < 0 || pid >= a.n_pages) {
+    if (u == 0) set_error(a.err, DERR_INDEX);
+    return;
+  }
+  const size_t dst = ((size_t)pid * a.Hkv * page + (slot - j * page)) * d;
+  const size_t hstep = (size_t)page * d;
+  float c[P], s[P];
+  if (ROPE && turns) {
+    const Axes ax{a.n_axes, {a.axis_pairs[0], a.axis_pairs[1], a.axis_pairs[2]}};
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int p = p0 + i;
+      c[i] = 1.f;
+      s[i] = 0.f;
+      if (p < half) {
+        const float2 cs = turn<false>((double)a.pos[(size_t)ax.of(p) * a.T + row] * a.freq[p]);
+        c[i] = cs.x * a.mag;
+        s[i] = cs.y * a.mag;
+      }
+    }
+  }
+  T* kp = (T*)a.kp + dst;
+  T* vp = (T*)a.vp + dst;
+  for (int h0 = blockIdx.y; h0 < a.Hkv; h0 += UN * gy) {
+    Batch nxt;
+    load(nxt, h0 + UN * gy);
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int h = h0 + i * gy;
+      if (h >= a.Hkv) continue;
+      if (MODE == kPair) {
+        if (!turns) {
+          kp[h * hstep + e0] = K[h * a.ksh + e0];
+        } else {
+          const float p = as_f32(K[h * a.ksh + e0]), q = as_f32(K[h * a.ksh + e1]);
+          kp[h * hstep + e0] = from_f32<T>(p * c[0] - q * s[0]);
+          kp[h * hstep + e1] = from_f32<T>(p * s[0] + q * c[0]);
+        }
+      } else {
+        if (ROPE && turns) {
+          float va[E], vb[E];
+          Vec<T>::unpack(cur.ka[i], va);
+          if (MODE == kInter) {
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+              const float p = va[2 * k], q = va[2 * k + 1];
+              va[2 * k] = p * c[k] - q * s[k];
+              va[2 * k + 1] = p * s[k] + q * c[k];
+            }
+          } else {
+            Vec<T>::unpack(cur.kb[i], vb);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+              const float p = va[k], q = vb[k];
+              va[k] = p * c[k] - q * s[k];
+              vb[k] = p * s[k] + q * c[k];
+            }
+            *reinterpret_cast<uint4*>(kp + h * hstep + e1) = Vec<T>::pack(vb);
+          }
+          cur.ka[i] = Vec<T>::pack(va);
+        }
+        *reinterpret_cast<uint4*>(kp + h * hstep + e0) = cur.ka[i];
+      }
+      if (f0 >= 0) *reinterpret_cast<uint4*>(vp + h * hstep + f0) = cur.va[i];
+      if (f1 >= 0) *reinterpret_cast<uint4*>(vp + h * hstep + f1) = cur.vb[i];
+    }
+    cur = nxt;
+  }
+}
+
+constexpr int kMeanThreads = 128;
+
+// grid (page slots that the call can touch, Hkv): tp slots per sequence, or (tp = 0) slots counted
+// sequence by sequence.
+template <typename T, int D>
+__global__ void __launch_bounds__(kMeanThreads) k_page_means(AppendArgs a, int tp) {
+  constexpr int E = 8, CH = D / E, RG = kMeanThreads / CH, UN = 8;
+  __shared__ float red[RG][D];
+  __shared__ int sm_find[kMeanThreads / 32 + 2];
+  const int tid = threadIdx.x, page = a.page;
+  // sequence b and its touched page: pages floor((len - n) / page) .. floor((len - 1) / page)
+  auto pages_of = [&](int b) -> int {
+    const int lo = min(max(a.q_start[b], 0), a.T);
+    const int n = max(0, min(a.q_start[b + 1], a.T) - lo);
+    const int len = min(max(a.kv_len[b], 0), a.max_pages * page);
+    if (n == 0 || len == 0) return 0;
+    return (len - 1) / page - max(len - n, 0) / page + 1;
+  };
+  int b, jt;
+  if (tp > 0) {
+    b = blockIdx.x / tp;
+    jt = blockIdx.x - b * tp;
+  } else {
+    const int lane = tid & 31, warp = tid >> 5;
+    const int run = (a.B + kMeanThreads - 1) / kMeanThreads;
+    const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+    int mine = 0;
+    for (int i = b0; i < b1; ++i) mine += pages_of(i);
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sm_find[warp] = inc;
+    __syncthreads();
+    int at = inc - mine;
+    for (int w = 0; w < warp; ++w) at += sm_find[w];
+    __syncthreads();
+    if (tid == 0) sm_find[0] = -1;
+    __syncthreads();
+    const int idx = blockIdx.x;
+    if (idx >= at && idx < at + mine) {
+      for (int i = b0; i < b1; ++i) {
+        const int c = pages_of(i);
+        if (idx < at + c) {
+          sm_find[0] = i;
+          sm_find[1] = idx - at;
+          break;
+        }
+        at += c;
+      }
+    }
+    __syncthreads();
+    b = sm_find[0];
+    jt = sm_find[1];
+    if (b < 0) return;
+  }
+  const int q0 = min(max(a.q_start[b], 0), a.T), n = max(0, min(a.q_start[b + 1], a.T) - q0);
+  const int len = min(max(a.kv_len[b], 0), a.max_pages * page);
+  const int j = max(len - n, 0) / page + jt, base = j * page, h = blockIdx.y;
+  if (n == 0 || base >= len) return;
+  const int pid = a.table[(size_t)b * a.max_pages + j];
+  if (pid < 0 || pid >= a.n_pages) return;        // recorded by k_cache_rows
+  const int rows = min(len - base, page);
+  const T* kp = (const T*)a.kp + ((size_t)pid * a.Hkv + h) * page * D;
+  const int c = tid % CH, rg = tid / CH;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the rows are in their slots
+  float acc[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] = 0.f;
+  for (int r = rg; r < rows; r += UN * RG) {
+    uint4 w[UN];
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+      if (r + i * RG < rows) Vec<T>::load(kp + (size_t)(r + i * RG) * D + c * E, w[i]);
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      if (r + i * RG >= rows) continue;
+      float v[E];
+      Vec<T>::unpack(w[i], v);
+#pragma unroll
+      for (int k = 0; k < E; ++k) acc[k] += v[k];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) red[rg][c * E + i] = acc[i];
+  __syncthreads();
+  if (tid < D) {
+    float s = 0.f;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) s += red[g][tid];
+    ((T*)a.km)[((size_t)pid * a.Hkv + h) * D + tid] = from_f32<T>(s / (float)rows);
+  }
+}
+
+template <typename T>
+cudaError_t launch_means(const AppendArgs& a, cudaStream_t st) {
+  // Page slots: every sequence touches at most ceil((n - 1) / page) + 1 pages.  With the longest
+  // chunk's number for each sequence a block finds its page without counting the others' (the
+  // shortest way for single tokens); unequal chunks would leave most of those slots empty, and
+  // are counted.
+  const long long counted = (long long)a.T / a.page + 2ll * a.B;
+  long long tp = ceil_div64((long long)a.max_chunk - 1, a.page) + 1;
+  if (tp > a.max_pages) tp = a.max_pages;
+  long long slots = tp * a.B;
+  if (slots > 2 * counted) {
+    tp = 0;
+    slots = counted < a.T ? counted : a.T;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)slots, a.Hkv);
+  cfg.blockDim = dim3(kMeanThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};                     // begins while the rows kernel runs, and waits for it
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return a.d == 64 ? cudaLaunchKernelEx(&cfg, k_page_means<T, 64>, a, (int)tp)
+                   : cudaLaunchKernelEx(&cfg, k_page_means<T, 128>, a, (int)tp);
 }
 
 template <typename T, int MODE, bool ROPE>
 cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t st) {
-  const int half = ROPE ? a.rot / 2 : 0;
-  const int rg = kAppThreads / RowUnits<T, MODE>::count(a.d, ROPE ? a.rot : 0);
-  const size_t sm = (size_t)a.page * half * 8 + (size_t)rg * a.d * 4;
-  auto kern = k_cache_append<T, MODE, ROPE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-  if (e != cudaSuccess) return e;
-  // every sequence touches at most ceil((n - 1) / page) + 1 pages; at least two blocks per SM,
-  // then as many heads per block as that leaves, to share the angles
-  long long slots = (long long)a.T / a.page + 2ll * a.B;
-  slots = slots < a.T ? slots : a.T;
-  int hpb = (int)(slots * a.Hkv / (2 * 148));
-  hpb = hpb < 1 ? 1 : (hpb > a.Hkv ? a.Hkv : hpb);
-  kern<<<dim3((unsigned)slots, ceil_div(a.Hkv, hpb)), kAppThreads, sm, st>>>(a, hpb);
-  return cudaGetLastError();
+  const long long units = (long long)a.T * RowUnits<T, MODE>::count(a.d, ROPE ? a.rot : 0);
+  const long long blocks = ceil_div64(units, kRopeThreads);
+  // Heads are dealt to 256 blocks: 4 x 1,024 tokens of 16 heads take 19.0 us that way (8 heads per
+  // thread), 21.3 us with 128 and 25.4 us with 1,024, where the angles serve two heads only.
+  long long hs = ceil_div64(256, blocks);
+  hs = hs < a.Hkv ? hs : a.Hkv;
+  k_cache_rows<T, MODE, ROPE><<<dim3((unsigned)blocks, (unsigned)hs), kRopeThreads, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_means<T>(a, st);
 }
 
 template <typename T>
