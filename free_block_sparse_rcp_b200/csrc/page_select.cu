@@ -5,232 +5,332 @@
 //   heads of the key/value head; the first n_sink and last n_recent visible pages are kept and
 //   the best scores fill the list up to n_select, ties to the lowest page.
 //
-// The list is decided by comparisons, so the scores are summed in 64 bits: in 32 bits the order
-// of the sum would decide between pages closer than 2^-24, and with a thousand pages the pair
-// at the border is that close in about one list of 10^4.
-// A 16-bit element becomes a double without a conversion instruction (those run at a quarter of
-// the double multiply-add rate): its exponent and mantissa are shifted into the double's
-// fields, which gives x 2^-kBias exactly (subnormals included), and the other factor, qbar,
-// carries 2^kBias.  The range holds: |qbar| <= 65504 for fp16 (2^16 2^1008 = 2^1024 is not
-// reached) and 2^128 2^896 = 2^1024 likewise for finite bf16 means.
+// The list is decided by comparisons, so it is the one of scores summed in 64 bits: in 32 bits
+// the order of the sum would decide between pages closer than 2^-24, and with a thousand pages
+// the pair at the border is that close in about one list of 10^4.  The scores are made in 32
+// bits all the same, with a bound on their error: every score s is off by at most
+// eps = 2^-19 max_j sum |qbar||kbar_j| (16 products in a lane's chain, 3 sums across lanes, the
+// rounding of qbar: 20 steps of 2^-24, and 32 are counted).  With t the n-th best score in 32
+// bits, a page above t + 2 eps is in the list and one below t - 2 eps is not, whatever the
+// errors; only the pages between (mostly the n-th itself) are scored again in 64 bits.  All in 64
+// bits cost 8 integer instructions per element to widen the 16-bit means and took 40 us for 256
+// lists of up to 1,024 pages.
 //
-// Work: the means are read once per unit (bytes: 1 / page of the keys'), 2 d operations per
-// page; the queries once.  One block per (unit, head), or several that share its pages when
-// there are few units; the selection then runs as a second kernel over the stored scores.
+// Work: the means are read once per unit (1 / page of the keys' bytes), 4 d operations per page;
+// the queries once.  One block per (unit, head), or several that share its pages when there are
+// few units; the selection then runs as a second kernel over the stored scores.
 #include "paged.cuh"
 
 namespace spr {
 namespace {
 
-constexpr int kSelThreads = 256;
+using paged::unpack2;
+
+constexpr int kSelThreads = 512;
 constexpr int kSelBins = 2048;
-constexpr int kSelSmemPages = 8192;   // scores kept in shared memory up to this many pages (64 KB)
+constexpr int kSelSmemPages = 8192;   // scores and keys in shared memory up to this many pages (96 KB)
+constexpr int kSelExact = 64;         // pages scored again in one step
 
+// largest exponent field of a packed pair's halves, as a bit pattern: >= kInf: not finite
 template <typename T>
-struct Wide;   // exponent field offset of the shifted 16-bit element
+struct InfBits;
 template <>
-struct Wide<__nv_bfloat16> {
-  static constexpr int shift = 13, bias = 896;       // 1023 - 127
-  static constexpr uint32_t inf = 0x7f80u;
+struct InfBits<__nv_bfloat16> {
+  static constexpr uint32_t v = 0x7f80u;
 };
 template <>
-struct Wide<__half> {
-  static constexpr int shift = 10, bias = 1008;      // 1023 - 15
-  static constexpr uint32_t inf = 0x7c00u;
+struct InfBits<__half> {
+  static constexpr uint32_t v = 0x7c00u;
 };
-// x 2^-bias of a finite 16-bit element
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
 template <typename T>
-__device__ __forceinline__ double wide(uint32_t e) {
-  return __hiloint2double((int)(((e & 0x7fffu) << Wide<T>::shift) | ((e & 0x8000u) << 16)), 0);
-}
-template <typename T>
-__device__ __forceinline__ bool not_finite(uint32_t w) {   // either half of a packed pair
-  return (w & Wide<T>::inf) == Wide<T>::inf || ((w >> 16) & Wide<T>::inf) == Wide<T>::inf;
-}
-__device__ __forceinline__ double pow2(int e) { return __hiloint2double((1023 + e) << 20, 0); }   // |e| <= 1022
+__device__ __forceinline__ bool finite2(uint32_t m) { return (m & 0xffffu) < InfBits<T>::v && (m >> 16) < InfBits<T>::v; }
 
-// Order of scores as unsigned integers (larger score, larger key); NaN is the lowest.
-__device__ __forceinline__ unsigned long long order_key(double x) {
-  if (!(x == x)) return 0ull;
-  const long long b = __double_as_longlong(x + 0.0);   // -0 becomes +0
+// Order of scores as unsigned integers (larger score, larger key; keys of numbers are above 0).
+__device__ __forceinline__ uint32_t order32(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);         // -0 becomes +0
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value32(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ unsigned long long order64(double x) {
+  const long long b = __double_as_longlong(x + 0.0);
   return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
 }
+
+// eps of the file's head from max_j sum |qbar||kbar_j| (2^-140: products below fp32's range)
+__device__ __forceinline__ float error_bound(float e) { return fmaf(e, 1.9073486328125e-6f, 7.2e-43f); }
 
 struct UnitInfo {
   int b, len, ntok, tok0, vis;   // tok0: packed row of the unit's first token; vis: visible pages
 };
 
 __device__ __forceinline__ bool unit_of(const SelectArgs& a, int idx, int* sm, UnitInfo& u) {
-  const int2 it = paged::find_item<paged::kUnits, kSelThreads>(a.q_start, a.B, a.T, idx, 1, 1, a.q_block, 1, sm);
-  if (it.x < 0) return false;
-  u.b = it.x;
-  const int q0 = min(max(a.q_start[it.x], 0), a.T);
-  const int n = max(0, min(a.q_start[it.x + 1], a.T) - q0);
-  const int lenr = a.kv_len[it.x];
-  u.len = min(max(lenr, 0), a.max_pages * a.page);
-  if (lenr != u.len && threadIdx.x == 0) set_error(a.err, DERR_INDEX);
-  const int t0 = it.y * a.q_block;     // < n
-  u.ntok = min(a.q_block, n - t0);
-  u.tok0 = q0 + t0;
-  const int end = paged::visible_end(u.len - n + t0 + u.ntok - 1, a.frame, u.len);
-  u.vis = (end + a.page - 1) / a.page;
+  const paged::Found f = paged::find_item<paged::kUnits, kSelThreads>(a.p, idx, 1, 1, sm);
+  if (f.b < 0) return false;
+  const paged::Seq s = paged::make_seq(a.p, f.b, f.lo, f.hi, f.len);
+  if (s.bad && threadIdx.x == 0) set_error(a.p.err, DERR_INDEX);
+  u.b = f.b;
+  u.len = s.len;
+  const int t0 = f.rank * a.p.q_block;     // < n
+  u.ntok = min(a.p.q_block, s.n - t0);
+  u.tok0 = s.q0 + t0;
+  const int end = paged::visible_end(s.len - s.n + t0 + u.ntok - 1, a.p.frame, s.len);
+  u.vis = (end + a.p.page - 1) / a.p.page;
   return true;
 }
 
-// Writes the list of one (unit, head) from its order keys (all threads of the block).
-__device__ void select_list(const unsigned long long* keys, int vis, int n_sink, int n_recent, int K, int* out, int* cnt,
-                            int* hist /* [kSelBins] */) {
-  __shared__ unsigned long long s_lo, s_hi;
-  __shared__ int s_warp[kSelThreads / 32], s_tie[kSelThreads / 32], s_bin, s_above, s_inbin;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int f0 = min(n_sink, vis), f1 = max(f0, vis - n_recent);   // free pages [f0, f1)
-  const int nfree = f1 - f0;
-  const int total = min(K, vis);
-  int want = total - (vis - nfree);        // free pages to take (>= 0: kept pages fit the list)
-  // every key above `hi` is taken and none below `lo`; `want` of those in [lo, hi] are.  The
-  // range is narrowed to one of 2048 equal parts per round until all of it or one value is
-  // wanted: at most six rounds for 64 bits.
-  unsigned long long lo = 0ull, hi = ~0ull;
-  bool all = want >= nfree;
-  if (!all && want > 0) {
-    if (tid == 0) { s_lo = ~0ull; s_hi = 0ull; }
+// Exclusive scan over the block (all threads), total in `total`.
+__device__ __forceinline__ int sel_scan(int v, int* sm /* [kSelThreads / 32] */, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) sm[warp] = inc;
+  __syncthreads();
+  int base = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) {
+    if (w < warp) base += sm[w];
+    sum += sm[w];
+  }
+  total = sum;
+  __syncthreads();
+  return base + inc - v;
+}
+
+struct PickShared {
+  int scan[kSelThreads / 32], bin, above, inbin, nfound;
+  unsigned long long lo, hi;
+  int list[kSelExact];
+  unsigned long long exact[kSelExact];
+  int in[kSelExact];
+};
+
+// The n-th largest key of keys[f0 .. f1) (1 <= n <= f1 - f0): the range [lo, hi] that holds it is
+// narrowed to one of 2048 equal parts per round, until one value is left.  want: on return how
+// many keys of that value are among the n.
+template <typename K>
+__device__ K nth_key(const K* keys, int f0, int f1, int& want, int* hist, PickShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) { sh.lo = ~0ull; sh.hi = 0ull; }
+  __syncthreads();
+  K mn = ~(K)0, mx = 0;
+  for (int j = f0 + tid; j < f1; j += kSelThreads) {
+    const K k = keys[j];
+    mn = k < mn ? k : mn;
+    mx = k > mx ? k : mx;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const K p = __shfl_xor_sync(0xffffffffu, mn, o), q = __shfl_xor_sync(0xffffffffu, mx, o);
+    mn = p < mn ? p : mn;
+    mx = q > mx ? q : mx;
+  }
+  if (lane == 0) {
+    atomicMin(&sh.lo, (unsigned long long)mn);
+    atomicMax(&sh.hi, (unsigned long long)mx);
+  }
+  __syncthreads();
+  K lo = (K)sh.lo, hi = (K)sh.hi;
+  constexpr int PER = kSelBins / kSelThreads;
+  while (lo < hi) {
+    const unsigned long long span = (unsigned long long)hi - (unsigned long long)lo;
+    const int bits = 64 - __clzll((long long)span);
+    const int s = bits > 11 ? bits - 11 : 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) hist[tid + i * kSelThreads] = 0;
     __syncthreads();
-    unsigned long long mn = ~0ull, mx = 0ull;
-    for (int j = f0 + tid; j < f1; j += kSelThreads) {
-      const unsigned long long k = keys[j];
-      mn = k < mn ? k : mn;
-      mx = k > mx ? k : mx;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long p = __shfl_xor_sync(0xffffffffu, mn, o), q = __shfl_xor_sync(0xffffffffu, mx, o);
-      mn = p < mn ? p : mn;
-      mx = q > mx ? q : mx;
-    }
-    if (lane == 0) {
-      atomicMin(&s_lo, mn);
-      atomicMax(&s_hi, mx);
+    for (int j0 = f0; j0 < f1; j0 += kSelThreads) {
+      const int j = j0 + tid;
+      int bin = -1;
+      if (j < f1) {
+        const K k = keys[j];
+        if (k >= lo && k <= hi) bin = (int)((k - lo) >> s);
+      }
+      const unsigned same = __match_any_sync(0xffffffffu, bin);
+      if (bin >= 0 && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
     }
     __syncthreads();
-    lo = s_lo;
-    hi = s_hi;
-    while (lo < hi) {
-      const unsigned long long span = hi - lo;
-      const int bits = 64 - __clzll((long long)span);
-      const int sh = bits > 11 ? bits - 11 : 0;
-      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int j0 = f0; j0 < f1; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        int bin = -1;
-        if (j < f1) {
-          const unsigned long long k = keys[j];
-          if (k >= lo && k <= hi) bin = (int)((k - lo) >> sh);
-        }
-        const unsigned same = __match_any_sync(0xffffffffu, bin);
-        if (bin >= 0 && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
-      }
-      __syncthreads();
-      // thread t owns bins 8 t' .. 8 t' + 7 from the top (t' = 255 - t)
-      constexpr int PER = kSelBins / kSelThreads;
-      const int top = kSelBins - 1 - tid * PER;
-      int mine = 0;
+    // thread t owns PER bins, from the top
+    const int top = kSelBins - 1 - tid * PER;
+    int mine = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) mine += hist[top - i];
-      int inc = mine;
+    for (int i = 0; i < PER; ++i) mine += hist[top - i];
+    int sum;
+    int above = sel_scan(mine, sh.scan, sum);
+    if (above < want && want <= above + mine) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (lane == 31) s_warp[warp] = inc;
-      __syncthreads();
-      int above = inc - mine;
-      for (int w = 0; w < warp; ++w) above += s_warp[w];
-      if (above < want && want <= above + mine) {
-        for (int i = 0; i < PER; ++i) {
-          const int c = hist[top - i];
-          if (want <= above + c) {
-            s_bin = top - i;
-            s_above = above;
-            s_inbin = c;
-            break;
-          }
-          above += c;
+      for (int i = 0; i < PER; ++i) {
+        const int c = hist[top - i];
+        if (above < want && want <= above + c) {
+          sh.bin = top - i;
+          sh.above = above;
         }
+        above += c;
       }
-      __syncthreads();
-      want -= s_above;
-      const unsigned long long nlo = lo + ((unsigned long long)s_bin << sh);
-      const unsigned long long width = (1ull << sh) - 1ull;
-      lo = nlo;
-      hi = hi - nlo < width ? hi : nlo + width;
-      const bool whole = want == s_inbin;
-      __syncthreads();
-      if (whole) {       // the whole bin is wanted: nothing in [lo, hi] is left out
-        all = true;
-        break;
-      }
+    }
+    __syncthreads();
+    want -= sh.above;
+    lo = lo + ((K)sh.bin << s);
+    const K width = (K)(((unsigned long long)1 << s) - 1ull);
+    hi = hi - lo < width ? hi : lo + width;
+    __syncthreads();
+  }
+  return lo;
+}
+
+// Score of page j in 64 bits by eight lanes (sub: lane of the eight); 0 for a page without one.
+template <typename T, int D>
+__device__ __forceinline__ unsigned long long exact_key(const SelectArgs& a, const UnitInfo& u, int h, int j,
+                                                        const double* q, int sub) {
+  const int pid = j >= 0 ? a.p.table[(size_t)u.b * a.p.max_pages + j] : -1;
+  const bool ok = pid >= 0 && pid < a.p.n_pages;
+  const T* row = (const T*)a.km + ((size_t)(ok ? pid : 0) * a.p.Hkv + h) * D;
+  double x = 0.;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    const uint4 w = *reinterpret_cast<const uint4*>(row + c * 64 + sub * 8);
+    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2<T>(p[i]);
+      x = fma((double)f.x, q[c * 64 + sub * 8 + 2 * i], x);
+      x = fma((double)f.y, q[c * 64 + sub * 8 + 2 * i + 1], x);
     }
   }
-  // ascending order: pages in steps of the block, positions by a scan
-  int base = 0, ties = 0;
-  const bool none = want <= 0 && !all;
-  for (int j0 = 0; j0 < vis; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    bool take = false, tie = false;
-    if (j < vis) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return ok && x == x ? order64(x) : 0ull;
+}
+
+// Writes the list of one (unit, head) from its 32-bit scores' keys (0: no score) and their error
+// bound (all threads of the block).  keys64: room for a 64-bit key per page.
+template <typename T, int D>
+__device__ void pick_list(const SelectArgs& a, const UnitInfo& u, int h, const uint32_t* keys, float eps, const double* q,
+                          unsigned long long* keys64, int* hist, int* out, int* cnt) {
+  __shared__ PickShared sh;
+  const int tid = threadIdx.x;
+  const int vis = u.vis, K = a.p.n_select;
+  const int f0 = min(a.n_sink, vis), f1 = max(f0, vis - a.n_recent);   // free pages [f0, f1)
+  const int nfree = f1 - f0, total = min(K, vis);
+  const int want = total - (vis - nfree);        // free pages to take (>= 0: kept pages fit the list)
+  const int per = (vis + kSelThreads - 1) / kSelThreads;
+  const int j0 = min(vis, tid * per), j1 = min(vis, j0 + per);      // this thread's run of pages
+  // in: key above `above`; undecided: [below, above]; take_all: all of those are in
+  uint32_t above = 0xffffffffu, below = 0u;
+  bool take_all = want >= nfree, exact = false;
+  int need = 0;                                  // undecided pages to take
+  int mine = 0;                                  // undecided pages of this thread's run
+  int first = 0, nund = 0;                       // their rank in the block, their number
+  if (!take_all && want > 0) {
+    int left = want;
+    const uint32_t t = nth_key<uint32_t>(keys, f0, f1, left, hist, sh);
+    if (t == 0u) {
+      above = below = 0u;                        // pages without a score are needed: the lowest ones
+    } else {
+      const float v = value32(t);
+      // an infinite score or bound leaves every page with a score undecided
+      const float up = v + 2.01f * eps, dn = v - 2.01f * eps;
+      above = up == up && fabsf(up) < INFINITY ? order32(up) : 0xffffffffu;
+      below = dn == dn && fabsf(dn) < INFINITY ? order32(dn) : 1u;
+    }
+    int nin = 0;
+    for (int j = max(j0, f0); j < min(j1, f1); ++j) {
+      const uint32_t k = keys[j];
+      nin += k > above;
+      mine += k <= above && k >= below;
+    }
+    int sum;
+    sel_scan(nin, sh.scan, sum);
+    need = want - sum;
+    first = sel_scan(mine, sh.scan, nund);
+    if (need == nund) {
+      take_all = true;
+    } else if (t == 0u) {
+      // by index
+    } else if (nund <= kSelExact) {
+      exact = true;
+      int at = first;
+      for (int j = max(j0, f0); j < min(j1, f1) && mine > 0; ++j)
+        if (keys[j] <= above && keys[j] >= below) sh.list[at++] = j;
+      __syncthreads();
+      const int i = tid >> 3;
+      const unsigned long long k = exact_key<T, D>(a, u, h, i < nund ? sh.list[i] : -1, q, tid & 7);
+      if ((tid & 7) == 0) sh.exact[i] = k;
+      __syncthreads();
+      if (tid < nund) {
+        int rank = 0;
+        for (int m = 0; m < nund; ++m) rank += sh.exact[m] > sh.exact[tid] || (sh.exact[m] == sh.exact[tid] && m < tid);
+        sh.in[tid] = rank < need;
+      }
+      __syncthreads();
+    } else {
+      // many undecided pages: their 64-bit keys, and the need-th of them
+      for (int jj = f0; jj < f1; jj += kSelThreads / 8) {
+        const int j = jj + (tid >> 3);
+        const bool und = j < f1 && keys[j] <= above && keys[j] >= below;
+        const unsigned long long k = exact_key<T, D>(a, u, h, und ? j : -1, q, tid & 7);
+        if (j < f1 && (tid & 7) == 0) keys64[j] = und ? (k > 0ull ? k : 1ull) : 0ull;
+      }
+      __syncthreads();
+      int ties = need;
+      const unsigned long long t64 = nth_key<unsigned long long>(keys64, f0, f1, ties, hist, sh);
+      // from here on the keys say in (2), tied (1) or out (0)
+      int m = 0;
+      for (int j = max(j0, f0); j < min(j1, f1); ++j) {
+        const unsigned long long k = keys64[j];
+        const int c = keys[j] > above ? 2 : (k > t64 ? 2 : (k == t64 ? 1 : 0));
+        m += c == 1;
+        keys64[j] = c;
+      }
+      first = sel_scan(m, sh.scan, nund);
+      need = ties;
+    }
+  }
+  const bool by64 = !take_all && want > 0 && !exact && !(above == 0u && below == 0u);
+  auto walk = [&](auto emit) {
+    int und = first;
+    for (int j = j0; j < j1; ++j) {
+      bool in;
       if (j < f0 || j >= f1) {
-        take = true;
-      } else if (!none) {
-        const unsigned long long k = keys[j];
-        take = k > hi || (all && k >= lo);
-        tie = !all && k >= lo && k <= hi;      // equal keys: the first `want` pages
+        in = true;
+      } else if (want <= 0) {
+        in = false;
+      } else if (by64) {
+        const int c = (int)keys64[j];
+        in = c == 2 || (c == 1 && und++ < need);
+      } else {
+        const uint32_t k = keys[j];
+        in = k > above || (take_all && k >= below);
+        if (!in && !take_all && k >= below) {
+          in = exact ? sh.in[und] != 0 : und < need;
+          ++und;
+        }
       }
+      if (in) emit(j);
     }
-    const unsigned mt = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) s_tie[warp] = __popc(mt);
-    __syncthreads();
-    int tb = ties;
-    for (int w = 0; w < warp; ++w) tb += s_tie[w];
-    if (tie && tb + __popc(mt & ((1u << lane) - 1u)) < want) take = true;
-    for (int w = 0; w < kSelThreads / 32; ++w) ties += s_tie[w];
-    const unsigned m = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) s_warp[warp] = __popc(m);
-    __syncthreads();
-    int at = base;
-    for (int w = 0; w < warp; ++w) at += s_warp[w];
-    at += __popc(m & ((1u << lane) - 1u));
-    if (take && at < total) out[at] = j;
-    for (int w = 0; w < kSelThreads / 32; ++w) base += s_warp[w];
-    __syncthreads();
-  }
+  };
+  int count = 0, sum;
+  walk([&](int) { ++count; });
+  int at = sel_scan(count, sh.scan, sum);
+  walk([&](int j) { out[at++] = j; });
   for (int i = total + tid; i < K; i += kSelThreads) out[i] = -1;
   if (tid == 0) *cnt = total;
 }
 
-// grid (units x splits, Hkv).  Scores of the split's share of the pages; with one split the
-// block goes on to the list.
+// The unit's mean query in 64 bits (NaN throughout if a query element is not finite).
 template <typename T, int D>
-__global__ void __launch_bounds__(kSelThreads) k_page_score(SelectArgs a) {
-  extern __shared__ __align__(16) unsigned char sm_sel[];
-  __shared__ int sm_find[kSelThreads / 32 + 2];
-  __shared__ double s_q[D];
-  __shared__ double s_red[kSelThreads / (D / 8)][D + 1];
-  const int tid = threadIdx.x, h = blockIdx.y;
-  const int unit = blockIdx.x / a.splits, split = blockIdx.x - unit * a.splits;
-  UnitInfo u;
-  if (!unit_of(a, unit, sm_find, u)) return;
-  const int G = a.Hq / a.Hkv;
-  constexpr int CH = D / 8;             // 16-byte chunks of a row
-  constexpr int RG = kSelThreads / CH;
-  // mean query, in the scaled domain until the last step
-  {
-    const int c = tid % CH, g0 = tid / CH;
+__device__ void mean_query(const SelectArgs& a, const UnitInfo& u, int h, double* q /* [D] */,
+                           double (*red)[D + 1] /* [kSelThreads / (D / 8)] */) {
+  constexpr int CH = D / 8, RG = kSelThreads / CH, UQ = 4;   // chunks of a row, rows per pass, passes in flight
+  const int tid = threadIdx.x, c = tid % CH, g0 = tid / CH, G = a.p.G, rows = u.ntok * G;
+  if (g0 < rows) {
     double s[8] = {0., 0., 0., 0., 0., 0., 0., 0.};
-    bool bad = false;
-    const int rows = u.ntok * G;
-    constexpr int UQ = 8;               // rows in flight
     for (int r = g0; r < rows; r += UQ * RG) {
       uint4 w[UQ];
 #pragma unroll
@@ -239,176 +339,213 @@ __global__ void __launch_bounds__(kSelThreads) k_page_score(SelectArgs a) {
         w[k] = make_uint4(0, 0, 0, 0);
         if (rr >= rows) continue;
         const int t = rr / G, gh = rr - t * G;
-        w[k] = *reinterpret_cast<const uint4*>((const T*)a.Q + (u.tok0 + t) * a.qst + (long long)(h * G + gh) * a.qsh + c * 8);
+        w[k] = *reinterpret_cast<const uint4*>((const T*)a.p.Q + (u.tok0 + t) * a.p.qst +
+                                               (long long)(h * G + gh) * a.p.qsh + c * 8);
       }
 #pragma unroll
       for (int k = 0; k < UQ; ++k) {
         const uint32_t p[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          bad |= not_finite<T>(p[i]);
-          s[2 * i] += wide<T>(p[i]);
-          s[2 * i + 1] += wide<T>(p[i] >> 16);
+          const float2 f = unpack2<T>(p[i]);
+          s[2 * i] += (double)f.x;
+          s[2 * i + 1] += (double)f.y;
         }
       }
     }
-    // a NaN or an infinity in a query row: every score of the unit is NaN
-    const double poison = bad ? __longlong_as_double(0x7ff8000000000000ll) : 0.0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_red[g0][c * 8 + i] = s[i] + poison;
-    __syncthreads();
-    if (tid < D) {
-      double t = 0.;
-      for (int g = 0; g < RG; ++g) t += s_red[g][tid];
-      // undo the shift of the sum (2^bias) and put 2^bias of the means' shift on qbar
-      t = t * pow2(Wide<T>::bias) / (double)((long long)u.ntok * G);
-      s_q[tid] = t * pow2(Wide<T>::bias);
-    }
-    __syncthreads();
+    for (int i = 0; i < 8; ++i) red[g0][c * 8 + i] = s[i];
   }
-  unsigned long long* keys = a.keys_global ? a.keys + ((size_t)unit * a.Hkv + h) * a.max_pages
-                                           : reinterpret_cast<unsigned long long*>(sm_sel + kSelBins * 4);
+  __syncthreads();
+  bool bad = false;
+  if (tid < D) {
+    double t = 0.;
+    const int groups = min(RG, rows);
+    for (int g = 0; g < groups; ++g) t += red[g][tid];
+    q[tid] = t / (double)rows;
+    bad = !(fabs(t) < INFINITY);       // an infinity or a NaN; sums of finite elements stay far below
+  }
+  if (__syncthreads_or(bad) && tid < D) q[tid] = __longlong_as_double(0x7ff8000000000000ll);
+  __syncthreads();
+}
+
+// grid (units x splits, Hkv).  Scores of the split's share of the pages; with one split the
+// block goes on to the list.
+template <typename T, int D>
+__global__ void __launch_bounds__(kSelThreads, 2) k_page_score(SelectArgs a) {
+  extern __shared__ __align__(16) unsigned char sm_sel[];
+  __shared__ int sm_find[kSelThreads / 32 + 8];
+  __shared__ double s_q[D];
+  __shared__ float s_eps[kSelThreads / 32];
+  const int tid = threadIdx.x, h = blockIdx.y;
+  const int unit = blockIdx.x / a.splits, split = blockIdx.x - unit * a.splits;
+  UnitInfo u;
+  if (!unit_of(a, unit, sm_find, u)) return;
+  int* hist = reinterpret_cast<int*>(sm_sel);
+  // the reduction of the mean query and, later, the keys share the space behind the bins
+  unsigned char* rest = sm_sel + kSelBins * 4;
+  mean_query<T, D>(a, u, h, s_q, reinterpret_cast<double(*)[D + 1]>(rest));
+  const size_t list = (size_t)unit * a.p.Hkv + h;
+  const bool stored = a.splits > 1 || a.keys_global;
+  uint32_t* keys = stored ? reinterpret_cast<uint32_t*>(a.scores) + list * a.p.max_pages
+                          : reinterpret_cast<uint32_t*>(rest);
   // eight lanes per page, D / 8 columns each
   constexpr int CPL = D / 8;
   const int sub = tid & 7;
-  double q[CPL];
+  float q[CPL];
+  // elements near the end of fp32's range lose their relative accuracy: then every score is
+  // decided in 64 bits
+  bool nan = false, tiny = false;
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) q[i] = s_q[(i / 8) * 64 + sub * 8 + (i & 7)];
+  for (int i = 0; i < CPL; ++i) {
+    const double v = s_q[(i / 8) * 64 + sub * 8 + (i & 7)];
+    q[i] = (float)v;
+    nan |= !(v == v);
+    tiny |= v != 0. && fabs(v) < 7.8886090522101181e-31;    // 2^-100
+  }
+  nan = __any_sync(0xffffffffu, nan);
+  tiny = __any_sync(0xffffffffu, tiny);
   const int p0 = (int)((long long)u.vis * split / a.splits), p1 = (int)((long long)u.vis * (split + 1) / a.splits);
   constexpr int PPB = kSelThreads / 8, UN = 4;   // pages of the block per step, steps in flight
-  const int* table = a.table + (size_t)u.b * a.max_pages;
-  // ids are loaded two rounds ahead of their scores, means one round
-  auto ids = [&](int j0, int* id) {
+  const int* table = a.p.table + (size_t)u.b * a.p.max_pages;
+  float eps = tiny ? INFINITY : 0.f;
+  int id[UN];
+#pragma unroll
+  for (int s = 0; s < UN; ++s) id[s] = p0 + s * PPB + (tid >> 3) < p1 ? table[p0 + s * PPB + (tid >> 3)] : -2;
+  for (int j0 = p0; j0 < p1; j0 += PPB * UN) {
+    uint4 w[UN][CPL / 8];
+    bool ok[UN];
 #pragma unroll
     for (int s = 0; s < UN; ++s) {
-      const int j = j0 + s * PPB + (tid >> 3);
-      id[s] = j < p1 ? table[j] : -2;
-    }
-  };
-  auto means = [&](const int* id, uint4 (*w)[CPL / 8]) {
-#pragma unroll
-    for (int s = 0; s < UN; ++s) {
-      if (id[s] < 0 || id[s] >= a.n_pages) continue;
-      const T* row = (const T*)a.km + ((size_t)id[s] * a.Hkv + h) * D;
+      ok[s] = id[s] >= 0 && id[s] < a.p.n_pages;
+      if (!ok[s] && id[s] != -2 && sub == 0) set_error(a.p.err, DERR_INDEX);
+      const T* row = (const T*)a.km + ((size_t)(ok[s] ? id[s] : 0) * a.p.Hkv + h) * D;
 #pragma unroll
       for (int c = 0; c < CPL / 8; ++c) w[s][c] = *reinterpret_cast<const uint4*>(row + c * 64 + sub * 8);
     }
-  };
-  int id0[UN], id1[UN];
-  uint4 w[UN][CPL / 8];
-  ids(p0, id0);
-  ids(p0 + PPB * UN, id1);
-  means(id0, w);
-  for (int j0 = p0; j0 < p1; j0 += PPB * UN) {
-    int id2[UN];
-    uint4 wn[UN][CPL / 8];
-    ids(j0 + 2 * PPB * UN, id2);
-    means(id1, wn);
+    // the next step's ids
+#pragma unroll
+    for (int s = 0; s < UN; ++s) {
+      const int j = j0 + (UN + s) * PPB + (tid >> 3);
+      id[s] = j < p1 ? table[j] : -2;
+    }
 #pragma unroll
     for (int s = 0; s < UN; ++s) {
       const int j = j0 + s * PPB + (tid >> 3);
-      const bool ok = id0[s] >= 0 && id0[s] < a.n_pages;
-      double x = 0.;
-      bool bad = !ok;
-      if (ok) {
+      float x = 0.f, e = 0.f;
+      uint32_t m = 0u;
 #pragma unroll
-        for (int c = 0; c < CPL / 8; ++c) {
-          const uint32_t p[4] = {w[s][c].x, w[s][c].y, w[s][c].z, w[s][c].w};
+      for (int c = 0; c < CPL / 8; ++c) {
+        const uint32_t p[4] = {w[s][c].x, w[s][c].y, w[s][c].z, w[s][c].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            bad |= not_finite<T>(p[i]);
-            x = fma(wide<T>(p[i]), q[c * 8 + 2 * i], x);
-            x = fma(wide<T>(p[i] >> 16), q[c * 8 + 2 * i + 1], x);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = unpack2<T>(p[i]);
+          m = max_abs2(m, p[i]);
+          x = fmaf(f.x, q[c * 8 + 2 * i], x);
+          x = fmaf(f.y, q[c * 8 + 2 * i + 1], x);
+          e = fmaf(fabsf(f.x), fabsf(q[c * 8 + 2 * i]), e);
+          e = fmaf(fabsf(f.y), fabsf(q[c * 8 + 2 * i + 1]), e);
         }
-      } else if (id0[s] != -2 && sub == 0) {
-        set_error(a.err, DERR_INDEX);
       }
-      if (bad) x = __longlong_as_double(0x7ff8000000000000ll);
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (j < p1 && sub == 0) keys[j] = order_key(x);
-    }
-#pragma unroll
-    for (int s = 0; s < UN; ++s) {
-      id0[s] = id1[s];
-      id1[s] = id2[s];
-#pragma unroll
-      for (int c = 0; c < CPL / 8; ++c) w[s][c] = wn[s][c];
+      for (int o = 4; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        e += __shfl_xor_sync(0xffffffffu, e, o);
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      }
+      if (j < p1) {
+        const bool scored = ok[s] && !nan && finite2<T>(m);
+        if (scored) eps = fmaxf(eps, fabsf(x) < INFINITY ? e : INFINITY);
+        // a finite page whose score overflows 32 bits is decided in 64 (the bound is infinite)
+        if (sub == 0) keys[j] = !scored ? 0u : (fabsf(x) < INFINITY ? order32(x) : 1u);
+      }
     }
   }
-  if (a.splits > 1) return;
+  eps = warp_max(eps);
+  if ((tid & 31) == 0) s_eps[tid >> 5] = eps;
   __syncthreads();
-  const size_t at = (size_t)unit * a.Hkv + h;
-  select_list(keys, u.vis, a.n_sink, a.n_recent, a.n_select, a.sel + at * a.n_select, a.cnt + at,
-              reinterpret_cast<int*>(sm_sel));
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) eps = fmaxf(eps, s_eps[w]);
+  if (stored) {
+    if (tid == 0) a.bounds[list * a.splits + split] = eps;
+    return;
+  }
+  pick_list<T, D>(a, u, h, keys, error_bound(eps), s_q,
+                  reinterpret_cast<unsigned long long*>(rest + (((size_t)a.p.max_pages * 4 + 15) & ~(size_t)15)), hist,
+                  a.sel + list * a.p.n_select, a.cnt + list);
 }
 
-// grid (units, Hkv): the lists from stored scores (moved to shared memory when they fit)
+// grid (units, Hkv): the lists from stored scores
+template <typename T, int D>
 __global__ void __launch_bounds__(kSelThreads) k_page_pick(SelectArgs a) {
   extern __shared__ __align__(16) unsigned char sm_sel[];
-  __shared__ int sm_find[kSelThreads / 32 + 2];
+  __shared__ int sm_find[kSelThreads / 32 + 8];
+  __shared__ double s_q[D];
   const int unit = blockIdx.x, h = blockIdx.y;
   UnitInfo u;
   if (!unit_of(a, unit, sm_find, u)) return;
-  const size_t at = (size_t)unit * a.Hkv + h;
-  const unsigned long long* keys = a.keys + at * a.max_pages;
-  if (u.vis <= kSelSmemPages) {
-    unsigned long long* mine = reinterpret_cast<unsigned long long*>(sm_sel + kSelBins * 4);
+  int* hist = reinterpret_cast<int*>(sm_sel);
+  unsigned char* rest = sm_sel + kSelBins * 4;
+  mean_query<T, D>(a, u, h, s_q, reinterpret_cast<double(*)[D + 1]>(rest));
+  const size_t list = (size_t)unit * a.p.Hkv + h;
+  const uint32_t* keys = reinterpret_cast<const uint32_t*>(a.scores) + list * a.p.max_pages;
+  unsigned long long* keys64 = a.keys + list * a.p.max_pages;
+  if (!a.keys_global) {
+    uint32_t* mine = reinterpret_cast<uint32_t*>(rest);
     for (int j = threadIdx.x; j < u.vis; j += kSelThreads) mine[j] = keys[j];
-    __syncthreads();
     keys = mine;
+    keys64 = reinterpret_cast<unsigned long long*>(rest + (((size_t)a.p.max_pages * 4 + 15) & ~(size_t)15));
   }
-  select_list(keys, u.vis, a.n_sink, a.n_recent, a.n_select, a.sel + at * a.n_select, a.cnt + at,
-              reinterpret_cast<int*>(sm_sel));
+  float eps = 0.f;
+  for (int s = 0; s < a.splits; ++s) eps = fmaxf(eps, a.bounds[list * a.splits + s]);
+  __syncthreads();
+  pick_list<T, D>(a, u, h, keys, error_bound(eps), s_q, keys64, hist, a.sel + list * a.p.n_select, a.cnt + list);
 }
 
 template <typename T, int D>
 cudaError_t launch_select_t(const SelectArgs& a, int* launches, cudaStream_t st) {
-  const int pages = a.max_pages < kSelSmemPages ? a.max_pages : kSelSmemPages;
-  const size_t sm = kSelBins * 4 + (size_t)pages * 8;
-  const size_t sm1 = a.splits > 1 ? 0 : (a.keys_global ? kSelBins * 4 : sm);
-  cudaError_t e = cudaFuncSetAttribute(k_page_score<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(kSelBins * 4 + kSelSmemPages * 8));
+  const size_t red = (size_t)(kSelThreads / (D / 8)) * (D + 1) * 8;
+  const size_t keys = (((size_t)a.p.max_pages * 4 + 15) & ~(size_t)15) + (size_t)a.p.max_pages * 8;
+  const bool stored = a.splits > 1 || a.keys_global;
+  const size_t all = kSelBins * 4 + (a.keys_global || keys < red ? red : keys), score = kSelBins * 4 + (stored ? red : all - kSelBins * 4);
+  cudaError_t e = cudaFuncSetAttribute(k_page_score<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)score);
   if (e != cudaSuccess) return e;
-  k_page_score<T, D><<<dim3((unsigned)a.units * a.splits, a.Hkv), kSelThreads, sm1, st>>>(a);
+  k_page_score<T, D><<<dim3((unsigned)a.units * a.splits, a.p.Hkv), kSelThreads, score, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   *launches = 1;
-  if (a.splits > 1) {
-    e = cudaFuncSetAttribute(k_page_pick, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kSelBins * 4 + kSelSmemPages * 8));
+  if (stored) {
+    e = cudaFuncSetAttribute(k_page_pick<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
     if (e != cudaSuccess) return e;
-    k_page_pick<<<dim3((unsigned)a.units, a.Hkv), kSelThreads, sm, st>>>(a);
+    k_page_pick<T, D><<<dim3((unsigned)a.units, a.p.Hkv), kSelThreads, all, st>>>(a);
     *launches = 2;
   }
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_select_d(const SelectArgs& a, int* launches, cudaStream_t st) {
-  return a.d == 64 ? launch_select_t<T, 64>(a, launches, st) : launch_select_t<T, 128>(a, launches, st);
+cudaError_t launch_select_d(const SelectArgs& a, int d, int* launches, cudaStream_t st) {
+  return d == 64 ? launch_select_t<T, 64>(a, launches, st) : launch_select_t<T, 128>(a, launches, st);
 }
 
 }  // namespace
 
-// Splits of a unit's pages: enough blocks for two per SM, at least 128 pages each (four steps
-// of a block).
+// Splits of a unit's pages: enough blocks for two per SM, at least 256 pages each (one step of a
+// block).
 SelectPlan select_plan(int units, int Hkv, int max_pages) {
   SelectPlan p{1, max_pages > kSelSmemPages};
   const long long blocks = (long long)units * Hkv;
   if (blocks > 0 && blocks < 148) {
     long long s = 296 / blocks;
-    const long long most = ceil_div(max_pages, 128);
+    const long long most = ceil_div(max_pages, 256);
     s = s < most ? s : most;
     p.splits = s < 1 ? 1 : (int)s;
   }
-  if (p.splits > 1) p.keys_global = true;
   return p;
 }
 
-cudaError_t launch_page_select(const SelectArgs& a, int* launches, cudaStream_t st) {
-  return a.dtype == SPARSEPR_FP16 ? launch_select_d<__half>(a, launches, st)
-                                  : launch_select_d<__nv_bfloat16>(a, launches, st);
+cudaError_t launch_page_select(const SelectArgs& a, int d, int dtype, int* launches, cudaStream_t st) {
+  return dtype == SPARSEPR_FP16 ? launch_select_d<__half>(a, d, launches, st)
+                                : launch_select_d<__nv_bfloat16>(a, d, launches, st);
 }
 
 }  // namespace spr

@@ -118,16 +118,18 @@ struct Seq {
   bool bad;
 };
 
-__device__ __forceinline__ Seq load_seq(const Args& a, int b) {
+__device__ __forceinline__ Seq make_seq(const Args& a, int b, int lo, int hi, int len) {
   Seq s;
   s.b = b;
-  const int lo = a.q_start[b], hi = a.q_start[b + 1], len = a.kv_len[b];
   const int cap = a.max_pages * a.page;
   s.q0 = min(max(lo, 0), a.T);
   s.n = max(0, min(hi, a.T) - s.q0);
   s.len = min(max(len, 0), cap);
   s.bad = lo < 0 || hi > a.T || hi < lo || len != s.len || s.n > a.max_chunk;
   return s;
+}
+__device__ __forceinline__ Seq load_seq(const Args& a, int b) {
+  return make_seq(a, b, a.q_start[b], a.q_start[b + 1], a.kv_len[b]);
 }
 
 // Items of a sequence with n new tokens.  Kinds: kWhole one item per sequence, kRows
@@ -141,22 +143,33 @@ __device__ __forceinline__ int item_count(int n, int G, int rows, int q_block, i
   return (int)(((long long)n + q_block - 1) / q_block) * ppu;
 }
 
-// Sequence and rank of item `idx` (counted sequence by sequence); every thread of the block
-// calls it, all get the result; b = -1 past the last item.  Each thread takes a run of
-// sequences, their counts are scanned, and the run that holds idx is walked by its thread.
+// Sequence and rank of item `idx` (counted sequence by sequence), with the sequence's raw entries;
+// every thread of the block calls it, all get the result; b = -1 past the last item.  Each thread
+// takes a run of sequences, their counts are scanned, and the run that holds idx is walked by its
+// thread.
+struct Found {
+  int b, rank, lo, hi, len;
+};
 template <int KIND, int NT>
-__device__ __forceinline__ int2 find_item(const int* __restrict__ q_start, int B, int T, int idx, int G, int rows,
-                                          int q_block, int ppu, int* sm /* [NT / 32 + 2] */) {
+__device__ __forceinline__ Found find_item(const Args& a, int idx, int rows, int ppu, int* sm /* [NT / 32 + 8] */) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (KIND == kWhole) return make_int2(idx < B ? idx : -1, 0);
-  const int run = (B + NT - 1) / NT;
-  const int b0 = min(B, tid * run), b1 = min(B, b0 + run);
-  auto count = [&](int b) -> int {
-    const int lo = min(max(q_start[b], 0), T);
-    return item_count<KIND>(max(0, min(q_start[b + 1], T) - lo), G, rows, q_block, ppu);
+  if (KIND == kWhole) {
+    if (idx >= a.B) return Found{-1, 0, 0, 0, 0};
+    return Found{idx, 0, a.q_start[idx], a.q_start[idx + 1], a.kv_len[idx]};
+  }
+  const int run = (a.B + NT - 1) / NT;
+  const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+  auto items = [&](int lo, int hi) -> int {
+    lo = min(max(lo, 0), a.T);
+    return item_count<KIND>(max(0, min(hi, a.T) - lo), a.G, rows, a.q_block, ppu);
   };
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += count(b);
+  int mine = 0, len0 = 0, lo0 = 0, hi0 = 0;
+  for (int b = b0; b < b1; ++b) {
+    lo0 = a.q_start[b];
+    hi0 = a.q_start[b + 1];
+    len0 = a.kv_len[b];
+    mine += items(lo0, hi0);
+  }
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -164,27 +177,33 @@ __device__ __forceinline__ int2 find_item(const int* __restrict__ q_start, int B
     if (lane >= o) inc += v;
   }
   if (lane == 31) sm[warp] = inc;
-  if (tid == 0) {
-    sm[NT / 32] = -1;
-    sm[NT / 32 + 1] = 0;
-  }
+  if (tid == 0) sm[NT / 32] = -1;
   __syncthreads();
-  int base = 0;
-  for (int w = 0; w < warp; ++w) base += sm[w];
-  int at = base + inc - mine;
+  int at = inc - mine;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w)
+    if (w < warp) at += sm[w];
   if (idx >= at && idx < at + mine) {
-    for (int b = b0; b < b1; ++b) {
-      const int c = count(b);
-      if (idx < at + c) {
-        sm[NT / 32] = b;
-        sm[NT / 32 + 1] = idx - at;
-        break;
-      }
+    int b = b0;
+    for (; b + 1 < b1; ++b) {
+      const int c = items(a.q_start[b], a.q_start[b + 1]);
+      if (idx < at + c) break;
       at += c;
     }
+    if (b + 1 < b1) {
+      lo0 = a.q_start[b];
+      hi0 = a.q_start[b + 1];
+      len0 = a.kv_len[b];
+    }
+    sm[NT / 32] = b;
+    sm[NT / 32 + 1] = idx - at;
+    sm[NT / 32 + 2] = lo0;
+    sm[NT / 32 + 3] = hi0;
+    sm[NT / 32 + 4] = len0;
   }
   __syncthreads();
-  return make_int2(sm[NT / 32], sm[NT / 32 + 1]);
+  const int* f = sm + NT / 32;
+  return Found{f[0], f[1], f[2], f[3], f[4]};
 }
 
 // Keys [0, end) that a token at position pos may see.
@@ -257,26 +276,22 @@ struct AppendArgs {
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
 
 struct SelectArgs {
-  const void* Q;
-  const int* q_start;
-  const int* kv_len;
-  const int* table;
+  paged::Args p;                  // Q, q_start, kv_len, table, err, sizes, strides
   const void* km;
   int* sel;
   int* cnt;
+  float* scores;                  // [units][Hkv][max_pages] and
+  float* bounds;                  // [units][Hkv][splits], used with splits > 1
   unsigned long long* keys;       // [units][Hkv][max_pages], used when `keys_global`
-  int* err;
-  int B, Hq, Hkv, d, dtype, page, n_pages, max_pages, T, frame, q_block, n_select, n_sink, n_recent;
-  int units, splits;
+  int n_sink, n_recent, units, splits;
   bool keys_global;
-  long long qst, qsh;
 };
 struct SelectPlan {
   int splits;
   bool keys_global;
 };
 SelectPlan select_plan(int units, int Hkv, int max_pages);
-cudaError_t launch_page_select(const SelectArgs& a, int* launches, cudaStream_t st);
+cudaError_t launch_page_select(const SelectArgs& a, int d, int dtype, int* launches, cudaStream_t st);
 
 // rows kernel: items of at most 16 * mt query rows on mma.sync; tile kernel: 256-row items on
 // tcgen05; combine: the join of split items.

@@ -210,7 +210,7 @@ int select_units(const sparsepr_cache_params& p) {
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Layout {
-  size_t part_lse, part_o, plan, plan_seq, plan_item, plan_pre, keys, total;
+  size_t part_lse, part_o, plan, plan_seq, plan_item, plan_pre, scores, bounds, keys, total;
 };
 Layout layout_of(const sparsepr_cache_params& p) {
   Layout L{};
@@ -230,11 +230,17 @@ Layout layout_of(const sparsepr_cache_params& p) {
   L.plan_seq = take(items ? (p.B + 1ull) * 4 : 0);
   L.plan_item = take(items * 4);
   L.plan_pre = take(items * p.Hkv * 8);
-  size_t keys = 0;
+  // selection: scores of split lists, and 64-bit keys of lists too long for shared memory
+  size_t scores = 0, bounds = 0, keys = 0;
   if (p.n_select > 0) {
-    const int units = select_units(p);
-    if (select_plan(units, p.Hkv, p.max_pages).keys_global) keys = (size_t)units * p.Hkv * p.max_pages * 8;
+    const size_t lists = (size_t)select_units(p) * p.Hkv;
+    const SelectPlan sp = select_plan(select_units(p), p.Hkv, p.max_pages);
+    if (sp.splits > 1 || sp.keys_global) scores = lists * p.max_pages * 4;
+    bounds = lists * sp.splits * 4;
+    if (sp.keys_global) keys = lists * p.max_pages * 8;
   }
+  L.scores = take(scores);
+  L.bounds = take(bounds);
   L.keys = take(keys);
   L.total = o;
   return L;
@@ -357,20 +363,24 @@ sparsepr_status sparsepr_page_select(const sparsepr_cache_params* p, const void*
   SPR_NONNULL(sel); SPR_NONNULL(sel_count);
   if (p->Hkv > 65535) return failv(SPARSEPR_EUNSUPPORTED, "more than 65535 key/value heads", p->Hkv);
   SelectArgs a{};
-  a.Q = Q; a.q_start = q_start; a.kv_len = kv_len; a.table = page_table; a.km = k_mean;
+  a.p.Q = Q; a.p.q_start = q_start; a.p.kv_len = kv_len; a.p.table = page_table;
+  a.p.err = at<int>(workspace, 0);
+  a.p.B = p->B; a.p.Hq = p->Hq; a.p.Hkv = p->Hkv; a.p.G = p->Hq / p->Hkv; a.p.page = p->page; a.p.n_pages = p->n_pages;
+  a.p.max_pages = p->max_pages; a.p.T = p->T; a.p.max_chunk = p->max_chunk; a.p.frame = p->frame;
+  a.p.q_block = p->q_block; a.p.n_select = p->n_select;
+  strides2(p->q_stride, p->Hq, p->d, a.p.qst, a.p.qsh);
+  a.km = k_mean;
   a.sel = sel; a.cnt = sel_count;
+  a.scores = at<float>(workspace, L.scores);
+  a.bounds = at<float>(workspace, L.bounds);
   a.keys = at<unsigned long long>(workspace, L.keys);
-  a.err = at<int>(workspace, 0);
-  a.B = p->B; a.Hq = p->Hq; a.Hkv = p->Hkv; a.d = p->d; a.dtype = p->dtype; a.page = p->page; a.n_pages = p->n_pages;
-  a.max_pages = p->max_pages; a.T = p->T; a.frame = p->frame;
-  a.q_block = p->q_block; a.n_select = p->n_select; a.n_sink = p->n_sink; a.n_recent = p->n_recent;
+  a.n_sink = p->n_sink; a.n_recent = p->n_recent;
   a.units = select_units(*p);
   const SelectPlan sp = select_plan(a.units, p->Hkv, p->max_pages);
   a.splits = sp.splits;
   a.keys_global = sp.keys_global;
-  strides2(p->q_stride, p->Hq, p->d, a.qst, a.qsh);
   int launches = 0;
-  const cudaError_t e = launch_page_select(a, &launches, (cudaStream_t)stream);
+  const cudaError_t e = launch_page_select(a, p->d, p->dtype, &launches, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "launch_page_select");
   set_launch_count(launches);
   return SPARSEPR_OK;

@@ -72,14 +72,14 @@ struct Item {
 
 template <int KIND, int NT>
 __device__ __forceinline__ bool load_item(const Args& a, int idx, int h, int* sm, Item& it) {
-  const int2 f = find_item<KIND, NT>(a.q_start, a.B, a.T, idx, a.G, 0, a.q_block, 1, sm);
-  if (f.x < 0) return false;
-  it.s = load_seq(a, f.x);
+  const Found f = find_item<KIND, NT>(a, idx, 0, 1, sm);
+  if (f.b < 0) return false;
+  it.s = make_seq(a, f.b, f.lo, f.hi, f.len);
   it.bad = it.s.bad;
   it.list = nullptr;
   it.cnt = 0;
   if (KIND == kUnits) {
-    it.tok0 = f.y * a.q_block;
+    it.tok0 = f.rank * a.q_block;
     it.ntok = min(a.q_block, it.s.n - it.tok0);
     const size_t at = (size_t)idx * a.Hkv + h;
     it.list = a.sel + at * a.n_select;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
   constexpr float SHIFT = ProbShift<T>::v;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint64_t s_full[ST], s_empty[ST];
-  __shared__ int s_abort, s_bad, s_find[NT / 32 + 2];
+  __shared__ int s_abort, s_bad, s_find[NT / 32 + 8];
   __shared__ float s_m[MT][4][16], s_l[MT][4][16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int idx = blockIdx.x, h = blockIdx.y;
@@ -388,7 +388,7 @@ constexpr int kCombThreads = 256;
 
 template <typename T, int D, int KIND>
 __global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int max_rows) {
-  __shared__ int s_find[kCombThreads / 32 + 2];
+  __shared__ int s_find[kCombThreads / 32 + 8];
   const int idx = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Item it;
   if (!load_item<KIND, kCombThreads>(a, idx, h, s_find, it)) return;

@@ -570,6 +570,41 @@ def test_select_ties_and_nan(spr, gpu):
     assert 8 not in sel[0, 0].tolist() and cnt.item() == 399
 
 
+@pytest.mark.parametrize("n_pages", [300, 3000])
+@pytest.mark.parametrize("kind", ["near", "tied", "tiny", "huge", "inf_query", "inf_mean"])
+def test_select_scores_that_32_bits_cannot_order(spr, gpu, kind, n_pages):
+    """Scores closer than the 32-bit sums are exact, hundreds of equal ones, values at the ends of
+    the range, and infinities: the lists are still those of the 64-bit scores."""
+    d, page = 64, 16
+    g = gen(26)
+    s = Scene(spr, gpu, [1], [16 * n_pages], Hq=2, Hkv=2, d=d, page=page, dt=BF, q_block=1, n_select=57, n_sink=1, n_recent=1, seed=27)
+    base = torch.randn(2, d, generator=g)
+    km = base.expand(s.n_pages, 2, d).clone()
+    if kind == "near":        # one small element tells the pages apart
+        km[:, :, 5] = 2.0 ** -12 * torch.rand(s.n_pages, 2, generator=g)
+    if kind == "tiny":
+        km = torch.randn(s.n_pages, 2, d, generator=g) * 1e-36
+        s.Q *= 2.0 ** -110
+    if kind == "huge":
+        km = torch.randn(s.n_pages, 2, d, generator=g) * 1e37
+        s.Q *= 50
+    if kind in ("inf_query", "inf_mean"):
+        km = torch.randn(s.n_pages, 2, d, generator=g)
+    s.km = km.to(BF)
+    if kind == "inf_query":
+        s.Q[0, 1, 3] = float("inf")
+    if kind == "inf_mean":
+        s.km[torch.randperm(s.n_pages, generator=g)[:n_pages - 20], :, 7] = float("-inf")
+    s.dev["km"], s.dev["Q"] = s.km.to(gpu), s.Q.to(gpu)
+    sel, cnt = s.select()
+    # a page or a query with an element that is not finite has no score: the lowest
+    km, Q = s.km.clone(), s.Q.clone()
+    km[~torch.isfinite(km).all(-1)] = float("nan")
+    Q[~torch.isfinite(Q).all(-1)] = float("nan")
+    want, wc = R.select(Q, s.new, s.kv, s.table, km, page, 1, 1, 57, 1, 1)
+    assert torch.equal(cnt.cpu(), wc) and torch.equal(sel.cpu(), want)
+
+
 @pytest.mark.parametrize("Hkv", [1, 160])
 def test_select_many_pages(spr, gpu, Hkv):
     """More pages than shared memory holds (scores in the workspace), one block per list or several."""
