@@ -107,13 +107,14 @@ struct PickShared {
   int scan[kSelThreads / 32], bin, above, inbin, nfound;
   unsigned long long lo, hi;
   int list[kSelExact];
-  unsigned long long exact[kSelExact];
+  unsigned long long exact[kSelExact];   // also the last candidates of nth_key
   int in[kSelExact];
 };
 
 // The n-th largest key of keys[f0 .. f1) (1 <= n <= f1 - f0): the range [lo, hi] that holds it is
-// narrowed to one of 2048 equal parts per round, until one value is left.  want: on return how
-// many keys of that value are among the n.
+// narrowed to one of 2048 equal parts per round, until one value or at most 64 keys are left,
+// which are ranked against each other.  want: n; on return how many keys of that value are among
+// the n.
 template <typename K>
 __device__ K nth_key(const K* keys, int f0, int f1, int& want, int* hist, PickShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31;
@@ -145,16 +146,11 @@ __device__ K nth_key(const K* keys, int f0, int f1, int& want, int* hist, PickSh
 #pragma unroll
     for (int i = 0; i < PER; ++i) hist[tid + i * kSelThreads] = 0;
     __syncthreads();
-    for (int j0 = f0; j0 < f1; j0 += kSelThreads) {
-      const int j = j0 + tid;
-      int bin = -1;
-      if (j < f1) {
-        const K k = keys[j];
-        if (k >= lo && k <= hi) bin = (int)((k - lo) >> s);
-      }
-      const unsigned same = __match_any_sync(0xffffffffu, bin);
-      if (bin >= 0 && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+    for (int j = f0 + tid; j < f1; j += kSelThreads) {
+      const K k = keys[j];
+      if (k >= lo && k <= hi) atomicAdd(&hist[(int)((k - lo) >> s)], 1);
     }
+    if (tid == 0) sh.nfound = 0;
     __syncthreads();
     // thread t owns PER bins, from the top
     const int top = kSelBins - 1 - tid * PER;
@@ -170,6 +166,7 @@ __device__ K nth_key(const K* keys, int f0, int f1, int& want, int* hist, PickSh
         if (above < want && want <= above + c) {
           sh.bin = top - i;
           sh.above = above;
+          sh.inbin = c;
         }
         above += c;
       }
@@ -179,7 +176,32 @@ __device__ K nth_key(const K* keys, int f0, int f1, int& want, int* hist, PickSh
     lo = lo + ((K)sh.bin << s);
     const K width = (K)(((unsigned long long)1 << s) - 1ull);
     hi = hi - lo < width ? hi : lo + width;
+    const int left = sh.inbin;
     __syncthreads();
+    if (left <= kSelExact) {
+      for (int j = f0 + tid; j < f1; j += kSelThreads) {
+        const K k = keys[j];
+        if (k >= lo && k <= hi) sh.exact[atomicAdd(&sh.nfound, 1)] = (unsigned long long)k;
+      }
+      __syncthreads();
+      if (tid < left) {
+        const unsigned long long k = sh.exact[tid];
+        int above = 0, same = 0;
+        for (int m = 0; m < left; ++m) {
+          above += sh.exact[m] > k;
+          same += sh.exact[m] == k;
+        }
+        if (above < want && want <= above + same) {     // all threads with this key write the same
+          sh.lo = k;
+          sh.above = above;
+        }
+      }
+      __syncthreads();
+      want -= sh.above;
+      lo = (K)sh.lo;
+      __syncthreads();
+      break;
+    }
   }
   return lo;
 }
