@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(NTT, 1)
   int* ints = reinterpret_cast<int*>(smem + L::oInt);   // [0] tmem base, [1] abort, [2..3] bad pages of a segment
   volatile int* abort_flag = ints + 1;
   volatile int* bad_page = ints + 2;
+  if (tid < 2) prefetch_tmap(tid ? &tmv : &tmk);
   if (tid == 0) {
     ints[1] = ints[2] = ints[3] = 0;
     mbar_init(su32(&bars->q), 64);
@@ -850,22 +851,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_tiles_join(Args a) {
 }  // namespace paged
 
 namespace {
-
-// launch that may begin while the kernel before it ends (it waits for its results itself)
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t sm, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = sm;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
 
 template <typename T, int D, bool SEL>
 cudaError_t tiles_t(const paged::Args& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {

@@ -465,18 +465,21 @@ __global__ void __launch_bounds__(kMeanThreads) k_page_means(AppendArgs a, int t
     __syncthreads();
     b = sm_find[0];
     jt = sm_find[1];
-    if (b < 0) return;
+    if (b < 0) {
+      asm volatile("griddepcontrol.wait;\n" ::: "memory");
+      return;
+    }
   }
   const int q0 = min(max(a.q_start[b], 0), a.T), n = max(0, min(a.q_start[b + 1], a.T) - q0);
   const int len = min(max(a.kv_len[b], 0), a.max_pages * page);
   const int j = max(len - n, 0) / page + jt, base = j * page, h = blockIdx.y;
-  if (n == 0 || base >= len) return;
-  const int pid = a.table[(size_t)b * a.max_pages + j];
+  const bool used = n > 0 && base < len;
+  const int pid = used ? a.table[(size_t)b * a.max_pages + j] : -1;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the rows are in their slots
   if (pid < 0 || pid >= a.n_pages) return;        // recorded by k_cache_rows
   const int rows = min(len - base, page);
   const T* kp = (const T*)a.kp + ((size_t)pid * a.Hkv + h) * page * D;
   const int c = tid % CH, rg = tid / CH;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the rows are in their slots
   float acc[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) acc[i] = 0.f;
@@ -519,17 +522,9 @@ cudaError_t launch_means(const AppendArgs& a, cudaStream_t st) {
     tp = 0;
     slots = counted < a.T ? counted : a.T;
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)slots, a.Hkv);
-  cfg.blockDim = dim3(kMeanThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};                     // begins while the rows kernel runs, and waits for it
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return a.d == 64 ? cudaLaunchKernelEx(&cfg, k_page_means<T, 64>, a, (int)tp)
-                   : cudaLaunchKernelEx(&cfg, k_page_means<T, 128>, a, (int)tp);
+  const dim3 grid((unsigned)slots, a.Hkv);
+  return a.d == 64 ? launch_early(k_page_means<T, 64>, grid, kMeanThreads, 0, st, a, (int)tp)
+                   : launch_early(k_page_means<T, 128>, grid, kMeanThreads, 0, st, a, (int)tp);
 }
 
 template <typename T, int MODE, bool ROPE>
