@@ -231,10 +231,10 @@ __device__ __forceinline__ int stream_limit(int end, const int* __restrict__ lis
   return (lo - 1) * page + (int)(in < 0 ? 0 : in < page ? in : page);
 }
 
-// Splits of an item whose stream has `tiles` tiles: split s of ns takes
+// Splits of an item whose stream has `tiles` tiles (at least min_split each): split s of ns takes
 // [tiles s / ns, tiles (s + 1) / ns).
 __device__ __forceinline__ int split_count(int tiles, int S, int min_split) {
-  const int n = (tiles + min_split - 1) / min_split;
+  const int n = tiles / min_split;
   return n < 1 ? 1 : (n < S ? n : S);
 }
 __device__ __forceinline__ int split_at(int tiles, int s, int ns) { return (int)((long long)tiles * s / ns); }

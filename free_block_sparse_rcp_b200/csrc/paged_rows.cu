@@ -227,13 +227,15 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
       ok = __all_sync(0xffffffffu, bounded_wait(su32(&s_full[st]), (i / ST) & 1, &s_abort, a.err));
       if (!ok) break;
       const uint32_t sk = base + st * 2 * C::kTile, sv = sk + C::kTile;
+      // even and odd steps of d in sums of their own: half the chain of dependent products
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float so[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         uint32_t b[4];
         ldsm4(b, sk + tile_off(kr, 2 * k + kc, BNR));
-        mma16816<T>(s[0], qf[k], b[0], b[1]);
-        mma16816<T>(s[1], qf[k], b[2], b[3]);
+        mma16816<T>(k & 1 ? so[0] : s[0], qf[k], b[0], b[1]);
+        mma16816<T>(k & 1 ? so[1] : s[1], qf[k], b[2], b[3]);
       }
       const int k0 = t * BNR + sl * 16;     // stream row of the slice's first key
       const bool edge = __any_sync(0xffffffffu, k0 + 16 > min(lim[0], lim[1]));
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float x = s[n][e] * a.scale_log2;
+          float x = (s[n][e] + so[n][e]) * a.scale_log2;
           if (edge && k0 + n * 8 + q2 + (e & 1) >= lim[e >> 1]) x = -INFINITY;
           s[n][e] = x;
           mx[e >> 1] = fmaxf(mx[e >> 1], x);
@@ -336,47 +338,48 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
       }
     }
     // every stage has landed and been read by all warps of all row tiles: the buffers are free
-    // (slices 1-3 of a row tile use 3 x 16 x D x 4 bytes)
+    // (a row tile uses 4 x 16 x D x 4 bytes); each warp adds a quarter of the columns
     named_sync(15, 128 * MT);
-    float4* buf = reinterpret_cast<float4*>(smem) + (size_t)mt * 3 * (D / 8) * 32;
-    if (sl > 0) {
+    float4* buf = reinterpret_cast<float4*>(smem) + (size_t)mt * 4 * (D / 8) * 32;
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-        buf[((size_t)(sl - 1) * (D / 8) + n) * 32 + lane] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
-    }
+    for (int n = 0; n < D / 8; ++n) buf[((size_t)sl * (D / 8) + n) * 32 + lane] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
     named_sync(1 + mt, 128);
-    if (sl == 0) {
-      const bool poison = !ok || s_bad != 0 || s_abort != 0;
+    const bool poison = !ok || s_bad != 0 || s_abort != 0;
+    float4 acc[D / 32];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = mt * 16 + g + 8 * r;
-        float inv = ls[r] > 0.f ? 1.f / ls[r] : 0.f;
-        float z = ls[r] > 0.f ? (ms[r] - SHIFT + log2f(ls[r])) * 0.69314718055994531f : -INFINITY;
-        if (!(ls[r] == ls[r]) || poison) inv = z = __int_as_float(0x7fffffff);
-        const int tok = row / a.G, gh = row - tok * a.G;
-        const long long qrow = it.s.q0 + it.tok0 + tok;
-        const int qh = h * a.G + gh;
-        const bool in = row < nrows;
-        const size_t prow = ((size_t)blockIdx.z * a.T + (in ? qrow : 0)) * a.Hq + qh;
-        T* op = (T*)a.O + (in ? qrow : 0) * a.ost + (long long)qh * a.osh;
+    for (int i = 0; i < D / 32; ++i) {
+      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          float x = o[n][2 * r], y = o[n][2 * r + 1];
+      for (int w = 0; w < 4; ++w) {
+        const float4 v = buf[((size_t)w * (D / 8) + sl * (D / 32) + i) * 32 + lane];
+        acc[i].x += v.x;
+        acc[i].y += v.y;
+        acc[i].z += v.z;
+        acc[i].w += v.w;
+      }
+    }
 #pragma unroll
-          for (int w = 0; w < 3; ++w) {
-            const float4 v = buf[((size_t)w * (D / 8) + n) * 32 + lane];
-            x += r ? v.z : v.x;
-            y += r ? v.w : v.y;
-          }
-          if (in) {
-            if (ns > 1) *reinterpret_cast<float2*>(a.part_o + prow * D + n * 8 + q2) = make_float2(x * inv, y * inv);
-            else *reinterpret_cast<uint32_t*>(op + n * 8 + q2) = pack2<T>(x * inv, y * inv);
-          }
-        }
-        if (in && (lane & 3) == 0) {
-          if (ns > 1) a.part_lse[prow] = z;
-          else if (a.lse) a.lse[qrow * a.Hq + qh] = z;
-        }
+    for (int r = 0; r < 2; ++r) {
+      const int row = mt * 16 + g + 8 * r;
+      if (row >= nrows) continue;
+      float inv = ls[r] > 0.f ? 1.f / ls[r] : 0.f;
+      float z = ls[r] > 0.f ? (ms[r] - SHIFT + log2f(ls[r])) * 0.69314718055994531f : -INFINITY;
+      if (!(ls[r] == ls[r]) || poison) inv = z = __int_as_float(0x7fffffff);
+      const int tok = row / a.G, gh = row - tok * a.G;
+      const long long qrow = it.s.q0 + it.tok0 + tok;
+      const int qh = h * a.G + gh;
+      const size_t prow = ((size_t)blockIdx.z * a.T + qrow) * a.Hq + qh;
+      T* op = (T*)a.O + qrow * a.ost + (long long)qh * a.osh;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int col = (sl * (D / 32) + i) * 8 + q2;
+        const float x = (r ? acc[i].z : acc[i].x) * inv, y = (r ? acc[i].w : acc[i].y) * inv;
+        if (ns > 1) *reinterpret_cast<float2*>(a.part_o + prow * D + col) = make_float2(x, y);
+        else *reinterpret_cast<uint32_t*>(op + col) = pack2<T>(x, y);
+      }
+      if (sl == 0 && (lane & 3) == 0) {
+        if (ns > 1) a.part_lse[prow] = z;
+        else if (a.lse) a.lse[qrow * a.Hq + qh] = z;
       }
     }
   }
@@ -402,27 +405,10 @@ __global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int max_
   for (int r = warp; r < nrows; r += kCombThreads / 32) {
     const int tok = r / a.G, qh = h * a.G + (r - tok * a.G);
     const size_t qrow = (size_t)it.s.q0 + it.tok0 + tok, prow = qrow * a.Hq + qh, step = (size_t)a.T * a.Hq;
-    // lane s holds the parts s and s + 32 (S <= 64)
-    float z[2], mx = -INFINITY;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      z[i] = lane + 32 * i < ns ? a.part_lse[prow + (lane + 32 * i) * step] : -INFINITY;
-      nan |= !(z[i] == z[i]);
-      mx = fmaxf(mx, z[i]);
-    }
-    mx = warp_max(mx);
-    nan = __any_sync(0xffffffffu, nan);
-    const float mu = mx == -INFINITY ? 0.f : mx;
-    const float w[2] = {expf(z[0] - mu), expf(z[1] - mu)};
-    float den = warp_sum(w[0] + w[1]);
-    float acc[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
     const float* po = a.part_o + prow * D + lane * (D / 32);
-    constexpr int UN = 8;               // parts in flight
-    for (int s0 = 0; s0 < ns; s0 += UN) {
-      float v[UN][D / 32];
+    constexpr int UN = 16;              // parts in flight; the first ones beside their lse
+    float v[UN][D / 32];
+    auto load = [&](int s0) {
 #pragma unroll
       for (int i = 0; i < UN; ++i) {
         if (s0 + i >= ns) continue;
@@ -439,6 +425,27 @@ __global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int max_
           v[i][1] = f.y;
         }
       }
+    };
+    load(0);
+    // lane s holds the lse of the parts s and s + 32 (S <= 64)
+    float z[2], mx = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      z[i] = lane + 32 * i < ns ? a.part_lse[prow + (lane + 32 * i) * step] : -INFINITY;
+      nan |= !(z[i] == z[i]);
+      mx = fmaxf(mx, z[i]);
+    }
+    mx = warp_max(mx);
+    nan = __any_sync(0xffffffffu, nan);
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    const float w[2] = {expf(z[0] - mu), expf(z[1] - mu)};
+    float den = warp_sum(w[0] + w[1]);
+    float acc[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+    for (int s0 = 0; s0 < ns; s0 += UN) {
+      if (s0 > 0) load(s0);
 #pragma unroll
       for (int i = 0; i < UN; ++i) {
         const int s = s0 + i;
