@@ -4,13 +4,17 @@
 // one stream of keys: the pages of their sequence, or of their unit's list, in order.  Two
 // 128-row tiles use every 128-key chunk that reaches shared memory, so the tensor cores work on
 // one tile while the other's softmax runs.
-//   warps 0-3, 4-7   softmax and epilogue of tile 0 and 1: thread r owns query row r = TMEM lane r
-//   warp 8           TMA: boxes of min(page, 128) rows of the pages of a chunk (K ring of 3, V
+//   warps 0-7, 8-15  softmax and epilogue of tile 0 and 1: two threads per query row r = TMEM lane r,
+//                    each with 32 of every 64 keys (a single warp per scheduler and tile stalls on
+//                    its own exponentials: 13 cycles per element against 8.4 with two)
+//   warp 16          TMA: boxes of min(page, 128) rows of the pages of a chunk (K ring of 3, V
 //                    ring of 2)
-//   warp 9           issues the MMAs
-//   warps 10-11      walk the CTA's work list and load the query rows
-// TMEM (512 columns): tile t holds S at 256 t and O at 256 t + 128; P overlays the first 64
-// columns of S as packed 16-bit pairs and is the second product's A operand.
+//   warp 17          issues the MMAs
+//   warps 18-19      walk the CTA's work list and load the query rows
+// TMEM (512 columns): S, O and P of both tiles, P as packed 16-bit pairs and the second product's A
+// operand.  With d = 128, S and O take all columns and P overlays the first 64 columns of its S, so
+// the next S waits for P V.  With d = 64 P has columns of its own: the next S starts as soon as the
+// softmax has read the last one, and its latency hides behind the second half's exponentials.
 // Everything a row may see is a prefix of the stream, so the mask is one comparison with the
 // row's limit in the chunks that straddle one.  Value rows of the last chunk past the item's
 // last visible key are zeroed in shared memory before their MMA: a page's unused slots may hold
@@ -36,7 +40,8 @@ namespace paged {
 using namespace spr::tc;
 
 constexpr int BM = 128, TPC = 2, BN = kPagedTileBN, KST = 3, VST = 2;
-constexpr int PROD_WARP = 8, MMA_WARP = 9, LOAD_WARP = 10, NTT = 384;
+constexpr int PROD_WARP = 16, MMA_WARP = 17, LOAD_WARP = 18, NTT = 640;
+constexpr int NSOFT = 256;             // softmax threads of a tile
 constexpr uint32_t kCols = 512;
 
 // What the roles of a CTA need to know about a piece of work.
@@ -53,7 +58,7 @@ struct Seg {
 
 struct TileBars {
   uint64_t q, qfree, kfull[KST], kempty[KST], vfull[VST], vempty[VST], vtail, s_full[TPC], p_full[TPC][2], pv_half[TPC],
-      o_done[TPC], o_free[TPC], seg_full[2], seg_free[2], mma_done;
+      pv_done[TPC], s_free[TPC], o_done[TPC], o_free[TPC], seg_full[2], seg_free[2], mma_done;
 };
 
 template <int D>
@@ -63,11 +68,12 @@ struct TileLayout {
   static constexpr uint32_t oK = oQ + TPC * kTile;
   static constexpr uint32_t oV = oK + KST * kTile;
   static constexpr uint32_t oBar = oV + VST * kTile;
-  static constexpr uint32_t oSeg = oBar + 256;
+  static constexpr uint32_t oSeg = oBar + 320;
   static constexpr uint32_t oInt = oSeg + 256;
-  static constexpr uint32_t kBytes = oInt + 64;
+  static constexpr uint32_t oEx = oInt + 64;                 // [tile][half][row] exchange of the row's threads
+  static constexpr uint32_t kBytes = oEx + TPC * 2 * BM * 4;
 };
-static_assert(sizeof(TileBars) <= 256 && 2 * sizeof(Seg) <= 256, "barrier and segment blocks");
+static_assert(sizeof(TileBars) <= 320 && 2 * sizeof(Seg) <= 256, "barrier and segment blocks");
 
 // Taking up an entry (its rows, the first softmax, the epilogue) costs about as much as two chunks:
 // an entry's cost begins with that many.
@@ -269,6 +275,15 @@ __device__ __forceinline__ void make_seg(const Args& a, long long e, int n_items
   g.nch0 = g.nrows <= BM ? g.nch : min(g.nch, max(0, (limit_of(BM - 1) + BN - 1) / BN - g.c0));
 }
 
+// TMEM columns of tile t
+template <int D>
+struct Tmem {
+  static constexpr bool kOwnP = D == 64;
+  static __device__ __forceinline__ uint32_t S(int t) { return kOwnP ? 128 * t : 256 * t; }
+  static __device__ __forceinline__ uint32_t O(int t) { return kOwnP ? 256 + 64 * t : 256 * t + 128; }
+  static __device__ __forceinline__ uint32_t P(int t) { return kOwnP ? 384 + 64 * t : 256 * t; }
+};
+
 // Instruction descriptor of kind::f16 for the element type (bits 7-9 and 10-12: 0 fp16, 1 bf16)
 template <typename T>
 __host__ __device__ constexpr uint32_t idesc_t(int M, int N, bool b_mn) {
@@ -310,13 +325,15 @@ __global__ void __launch_bounds__(NTT, 1)
     mbar_init(su32(&bars->vtail), 1);
     for (int t = 0; t < TPC; ++t) {
       mbar_init(su32(&bars->s_full[t]), 1);
-      mbar_init(su32(&bars->p_full[t][0]), 128);
-      mbar_init(su32(&bars->p_full[t][1]), 128);
+      mbar_init(su32(&bars->p_full[t][0]), NSOFT);
+      mbar_init(su32(&bars->p_full[t][1]), NSOFT);
       mbar_init(su32(&bars->pv_half[t]), 1);
+      mbar_init(su32(&bars->pv_done[t]), 1);
+      mbar_init(su32(&bars->s_free[t]), NSOFT);
       mbar_init(su32(&bars->o_done[t]), 1);
-      mbar_init(su32(&bars->o_free[t]), 128);
+      mbar_init(su32(&bars->o_free[t]), NSOFT);
       mbar_init(su32(&bars->seg_full[t]), 1);
-      mbar_init(su32(&bars->seg_free[t]), 256 + 3 * 32);   // softmax threads, TMA, MMA and the second load warp
+      mbar_init(su32(&bars->seg_free[t]), 2 * NSOFT + 3 * 32);   // softmax threads, TMA, MMA and the second load warp
     }
     mbar_init(su32(&bars->mma_done), 1);
     fence_barrier_init();
@@ -328,7 +345,7 @@ __global__ void __launch_bounds__(NTT, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = (uint32_t)ints[0];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, (uint32_t)ints[0], 0);   // known to be uniform: see below
   const uint32_t sQ = base + L::oQ, sK = base + L::oK, sV = base + L::oV;
   auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
     return bounded_wait(su32(&bar), parity, abort_flag, a.err);
@@ -514,7 +531,10 @@ __global__ void __launch_bounds__(NTT, 1)
     int use0 = 0, use1 = 0;           // segments with chunks of each tile so far
     Seg g;
     for (int i = 0; ok && get_seg(i, g); ++i) {
-      const int nch = g.nch, nch0 = g.nch0, ntile = g.nrows > BM ? 2 : 1;
+      // Broadcast, so that the compiler knows the counts to be the same in all lanes: descriptors
+      // derived from them then stay in uniform registers.
+      const int nch = __shfl_sync(0xffffffffu, g.nch, 0), nch0 = __shfl_sync(0xffffffffu, g.nch0, 0);
+      const int ntile = __shfl_sync(0xffffffffu, g.nrows > BM ? 2 : 1, 0);
       const int cn0 = nch0, cn1 = ntile > 1 ? nch : 0;
       __syncwarp();
       free_seg(i);
@@ -534,7 +554,7 @@ __global__ void __launch_bounds__(NTT, 1)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-          tc_mma_lead(lead, tmem + 256 * t, qd + off, kd + off, IDS, k > 0 ? 1u : 0u);
+          tc_mma_lead(lead, tmem + Tmem<D>::S(t), qd + off, kd + off, IDS, k > 0 ? 1u : 0u);
         }
         tc_commit_lead(lead, su32(&bars->s_full[t]));
         if (t == ntile - 1) {
@@ -543,28 +563,27 @@ __global__ void __launch_bounds__(NTT, 1)
         }
         return true;
       };
-      // O_t += P_t V_j, P from TMEM, half a chunk at a time; the last tile releases V_j
-      auto issue_pv = [&](int t, int j) -> bool {
+      // half hh of O_t += P_t V_j, P from TMEM; the last tile's second half releases V_j
+      auto issue_pv = [&](int t, int j, int hh) -> bool {
         const int vs = (kc + j) % VST;
         const uint64_t vd = sdesc(sV + vs * L::kTile, 16384, 1024);
         const int tc = t == 0 ? tc0 : tc1, use = t == 0 ? use0 : use1;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          if (!waits(bars->p_full[t][hh], (tc + j) & 1)) return false;
-          if (hh == 0) {
-            if (t == first_user(j) && !waits(bars->vfull[vs], ((kc + j) / VST) & 1)) return false;
-            // the previous segment's sums have been read
-            if (j == 0 && use > 0 && !waits(bars->o_free[t], (use - 1) & 1)) return false;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int k = 4 * hh; k < 4 * hh + 4; ++k)
-            tc_mma_ts_lead(lead, tmem + 256 * t + 128, tmem + 256 * t + k * 8, vd + k * 128, IDO,
-                           (j > 0 || k > 0) ? 1u : 0u);
-          if (hh == 0) tc_commit_lead(lead, su32(&bars->pv_half[t]));
+        if (!waits(bars->p_full[t][hh], (tc + j) & 1)) return false;
+        if (hh == 0) {
+          if (t == first_user(j) && !waits(bars->vfull[vs], ((kc + j) / VST) & 1)) return false;
+          // the previous segment's sums have been read
+          if (j == 0 && use > 0 && !waits(bars->o_free[t], (use - 1) & 1)) return false;
         }
-        if (t == ntile - 1) tc_commit_lead(lead, su32(&bars->vempty[vs]));
-        if (j + 1 == count(t)) tc_commit_lead(lead, su32(&bars->o_done[t]));
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_ts_lead(lead, tmem + Tmem<D>::O(t), tmem + Tmem<D>::P(t) + (4 * hh + k) * 8, vd + (4 * hh + k) * 128, IDO,
+                         (j > 0 || hh > 0 || k > 0) ? 1u : 0u);
+        tc_commit_lead(lead, su32(hh == 0 ? &bars->pv_half[t] : &bars->pv_done[t]));
+        if (hh == 1) {
+          if (t == ntile - 1) tc_commit_lead(lead, su32(&bars->vempty[vs]));
+          if (j + 1 == count(t)) tc_commit_lead(lead, su32(&bars->o_done[t]));
+        }
         return true;
       };
       if (nch == 0) tc_commit_lead(lead, su32(&bars->qfree));
@@ -573,8 +592,15 @@ __global__ void __launch_bounds__(NTT, 1)
       for (int j = 0; ok && j < nch; ++j) {
         for (int t = 0; ok && t < ntile; ++t) {
           if (j >= count(t)) continue;
-          ok = issue_pv(t, j);
-          if (ok && j + 1 < count(t)) ok = issue_s(t, j + 1);
+          const bool more = j + 1 < count(t);
+          ok = issue_pv(t, j, 0);
+          if (Tmem<D>::kOwnP && ok && more) {
+            ok = waits(bars->s_free[t], ((t == 0 ? tc0 : tc1) + j) & 1);
+            tc_fence_after();
+            ok = ok && issue_s(t, j + 1);
+          }
+          ok = ok && issue_pv(t, j, 1);
+          if (!Tmem<D>::kOwnP && ok && more) ok = issue_s(t, j + 1);
         }
       }
       kc += nch;
@@ -588,11 +614,15 @@ __global__ void __launch_bounds__(NTT, 1)
     __syncwarp();
   } else {
     // ---------------- softmax + epilogue ----------------
-    const int t = warp >> 2;
-    const int r = tid & (BM - 1);
+    const int t = warp >> 3, hv = (warp >> 2) & 1;     // tile; which 32 of every 64 keys
+    const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + 256 * t + lane_off, tO = tS + 128;
+    const uint32_t tS = tmem + Tmem<D>::S(t) + lane_off, tO = tmem + Tmem<D>::O(t) + lane_off,
+                   tP = tmem + Tmem<D>::P(t) + lane_off;
     const int row = t * BM + r;
+    const int pair = 1 + t * 4 + (warp & 3);           // named barrier of the two warps of these rows
+    float* mine = reinterpret_cast<float*>(smem + L::oEx) + (t * 2 + hv) * BM + r;
+    const float* other = reinterpret_cast<const float*>(smem + L::oEx) + (t * 2 + (hv ^ 1)) * BM + r;
     bool ok = true;
     int tc = 0, use = 0;              // chunks and segments of this tile so far
     Seg g;
@@ -608,10 +638,9 @@ __global__ void __launch_bounds__(NTT, 1)
       if (in && a.frame != 0)
         lim = min(g.total, stream_limit(visible_end(g.len - g.n + g.tok0 + (g.row0 + row) / a.G, a.frame, g.len), g.list,
                                         g.cnt, a.page));
-      float m_used = -INFINITY, l = 0.f;
+      float m_used = -INFINITY, l = 0.f;     // m_used: the same in both threads of a row
       const uint64_t sc2 = f2pack(a.scale_log2, a.scale_log2);
-      // 32 columns of S to probabilities against the running maximum; returns with the packed
-      // row sum in rs2
+      // 32 columns of S to probabilities against the running maximum, and their sums in rs2
       auto probs = [&](auto masked, const uint32_t* sr, uint32_t* pk, int left, uint64_t nmu2, uint64_t& rs2) {
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
@@ -627,85 +656,83 @@ __global__ void __launch_bounds__(NTT, 1)
           pk[c >> 1] = pack2<T>(p0, p1);
         }
       };
-      // half hh of chunk j against its own maximum: O is rescaled first
-      auto redo = [&](int j, int hh, int left, uint32_t* pk) {
-        uint32_t sr[32];
+      // half hh of chunk j against its own maximum (both threads of the rows): O is rescaled first,
+      // half its columns by each
+      auto redo = [&](int j, int hh, int left, const uint32_t* sr, uint32_t* pk) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          tc_ld32(tS + 64 * hh + 32 * q, sr);
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (32 * q + c < left) mx = fmaxf(mx, __uint_as_float(sr[c]));
-        }
+        for (int c = 0; c < 32; ++c)
+          if (c < left) mx = fmaxf(mx, __uint_as_float(sr[c]));
+        *mine = mx;
+        named_sync(pair, 64);
+        mx = fmaxf(mx, *other);
         const float m_new = fmaxf(m_used, mx * a.scale_log2);
         float alpha = 1.f;
         if (m_new > m_used) {
           alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - m_new);
           m_used = m_new;
         }
-        // the products of the earlier chunks completed before S_t,j did; those of this chunk's
-        // first half are waited for
-        if (hh == 1) ok = ok && __all_sync(0xffffffffu, wait(bars->pv_half[t], (tc + j) & 1));
+        // the products of the earlier chunks are complete (they were before S_t,j with d = 128, and
+        // have been waited for with d = 64); those of this chunk's first half are waited for
+        if (hh == 1) ok = ok && waits(bars->pv_half[t], (tc + j) & 1);
         if (j > 0 || hh == 1) {
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            tc_ld32(tO + c * 32, sr);
+          for (int c = 0; c < D / 32; ++c) {       // 16 columns
+            uint32_t o[16];
+            tc_ld16(tO + hv * (D / 2) + c * 16, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) sr[e] = __float_as_uint(__uint_as_float(sr[e]) * alpha);
-            tc_st32(tO + c * 32, sr);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc_st16(tO + hv * (D / 2) + c * 16, o);
           }
         }
         l *= alpha;
         const float mu = (m_used == -INFINITY) ? 0.f : m_used - SHIFT;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          tc_ld32(tS + 64 * hh + 32 * q, sr);
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float p0 = 32 * q + c < left ? ex2(__uint_as_float(sr[c]) * a.scale_log2 - mu) : 0.f;
-            const float p1 = 32 * q + c + 1 < left ? ex2(__uint_as_float(sr[c + 1]) * a.scale_log2 - mu) : 0.f;
-            l += p0 + p1;
-            pk[16 * q + (c >> 1)] = pack2<T>(p0, p1);
-          }
+        for (int c = 0; c < 32; c += 2) {
+          const float p0 = c < left ? ex2(__uint_as_float(sr[c]) * a.scale_log2 - mu) : 0.f;
+          const float p1 = c + 1 < left ? ex2(__uint_as_float(sr[c + 1]) * a.scale_log2 - mu) : 0.f;
+          l += p0 + p1;
+          pk[c >> 1] = pack2<T>(p0, p1);
         }
+        // P goes where the other thread's half of S may lie
+        named_sync(pair, 64);
       };
       for (int j = 0; j < nct; ++j) {
-        ok = __all_sync(0xffffffffu, wait(bars->s_full[t], (tc + j) & 1));
-        if (!ok) break;
+        ok = waits(bars->s_full[t], (tc + j) & 1);
+        // both warps of the rows take the same way out
+        if (!bar_and(pair, 64, ok)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const int valid = lim - (g.c0 + j) * BN;
-        const bool full = __all_sync(0xffffffffu, valid >= BN);
-        uint32_t ra[32], rb[32], pk[32];
-        tc_ld32_start(tS, ra);
-        tc_ld32_start(tS + 32, rb);
-        tc_ld32_wait(ra);
-        tc_ld32_wait(rb);
-        // one speculative pass of each half against the running maximum, kept while the half's
-        // row sum stays in range
+        const int valid = lim - (g.c0 + j) * BN - 32 * hv;
+        const bool full = __all_sync(0xffffffffu, valid >= 96);
+        // one speculative pass of each half against the running maximum, kept while the row sums
+        // of both threads stay in range
         auto chunk = [&](auto masked) {
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const int left = valid - 64 * hh;
-            const bool spec = __all_sync(0xffffffffu, m_used != -INFINITY);
+            uint32_t sr[32], pk[16];
+            tc_ld32(tS + 64 * hh + 32 * hv, sr);
+            if (Tmem<D>::kOwnP && hh == 1) {      // S has been read
+              tc_fence_before();
+              mbar_arrive(su32(&bars->s_free[t]));
+            }
             const float nm = SHIFT - m_used;
             const uint64_t nmu2 = f2pack(nm, nm);
             uint64_t rs2 = 0ull;
-            probs(masked, ra, pk, left, nmu2, rs2);
-            if (hh == 0) tc_ld32_start(tS + 64, ra);
-            probs(masked, rb, pk + 16, left - 32, nmu2, rs2);
-            if (hh == 0) tc_ld32_start(tS + 96, rb);
+            probs(masked, sr, pk, left, nmu2, rs2);
             float r0, r1;
             f2unpack(rs2, r0, r1);
-            const bool keep = spec && r0 + r1 <= ProbBound<T>::v;
-            if (hh == 0) {
-              tc_ld32_wait(ra);
-              tc_ld32_wait(rb);
-            }
-            if (__all_sync(0xffffffffu, keep)) l += r0 + r1;
-            else redo(j, hh, left, pk);
-            tc_st32(tS + 32 * hh, pk);
+            const bool keep = m_used != -INFINITY && r0 + r1 <= ProbBound<T>::v;
+            if (Tmem<D>::kOwnP && hh == 0 && tc + j > 0)      // P_j-1 has been used
+              ok = ok && waits(bars->pv_done[t], (tc + j - 1) & 1);
+            // also: both have read their half of S, which P may overlay
+            if (bar_and(pair, 64, keep)) l += r0 + r1;
+            else redo(j, hh, left, sr, pk);
+            tc_st16(tP + 32 * hh + 16 * hv, pk);
             tc_fence_before();
             mbar_arrive(su32(&bars->p_full[t][hh]));
           }
@@ -715,7 +742,12 @@ __global__ void __launch_bounds__(NTT, 1)
       }
       if (ok && nct > 0) ok = waits(bars->o_done[t], use & 1);
       tc_fence_after();
-      const bool poison = !ok || g.bad != 0 || bad_page[i & 1] != 0 || !(l == l);
+      // the row's sum over both threads (the exchange slots are free: the last use was read before
+      // the chunk's barrier)
+      *mine = ok ? l : __int_as_float(0x7fffffff);
+      named_sync(pair, 64);
+      l = hv ? *other + *mine : *mine + *other;
+      const bool poison = g.bad != 0 || bad_page[i & 1] != 0 || !(l == l);
       const float inv = poison ? __int_as_float(0x7fffffff) : (l > 0.f ? 1.f / l : 0.f);
       const float z = poison ? __int_as_float(0x7fffffff)
                              : (l > 0.f ? (m_used - SHIFT + log2f(l)) * 0.69314718055994531f : -INFINITY);
@@ -727,7 +759,8 @@ __global__ void __launch_bounds__(NTT, 1)
       // pieces are kept as [slot][d / 4][256 rows] groups of four, so that a warp's rows are adjacent
       float4* prt = reinterpret_cast<float4*>(a.part_o) + (size_t)(g.slot < 0 ? 0 : g.slot) * (D / 4) * kPagedTileRows + row;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int cc = 0; cc < D / 64; ++cc) {
+        const int c = hv * (D / 64) + cc;      // 32 columns
         uint32_t o[32];
         if (nct > 0 && ok) {
           tc_ld32(tO + c * 32, o);
@@ -735,7 +768,7 @@ __global__ void __launch_bounds__(NTT, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (c == D / 32 - 1 && nct > 0) {       // the sums have been read: the next segment may start its own
+        if (cc == D / 64 - 1 && nct > 0) {       // the sums have been read: the next segment may start its own
           tc_fence_before();
           mbar_arrive(su32(&bars->o_free[t]));
         }
@@ -747,20 +780,23 @@ __global__ void __launch_bounds__(NTT, 1)
                   make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
                               __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
           } else {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[e] = pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
             uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack2<T>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
       }
-      if (in) {
+      if (in && hv == 0) {
         if (g.slot >= 0) a.part_lse[prow] = z;
         else if (a.lse) a.lse[qrow * a.Hq + qh] = z;
       }
+      named_sync(pair, 64);      // the sums have been exchanged before the next segment's maxima
       tc += nct;
       use += nct > 0 ? 1 : 0;
       free_seg(i);
