@@ -429,46 +429,60 @@ def _torch():
     return _tc
 
 
-def _expect(name, t, shape, dtype, dev):
-    """t has this shape and type and lies on device number dev (-1: the CPU)."""
-    if t.shape == shape and t.dtype is dtype and t.get_device() == dev:
-        return
+def _refuse(check, name, t, shape, dtype, dev):
+    """Raises for a tensor that differs from what the params say (invalid params first)."""
+    _check(*check)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _elem(p):
-    dt = _torch().elem.get(p.dtype)
-    if dt is None:
-        raise ValueError(f"unknown dtype code {p.dtype}")
-    return dt
+def _pointers(validate, p, dev, specs):
+    """Addresses of contiguous tensors (name, tensor, shape, dtype) on device dev."""
+    out = []
+    for name, t, shape, dt in specs:
+        if t.shape != shape or t.dtype is not dt or t.get_device() != dev or not t.is_contiguous():
+            _refuse((validate(p), name), name, t, shape, dt, dev)
+        out.append(t.data_ptr())
+    return out
 
 
-def _strided(p, first, views):
-    """p, or a copy of it with the element strides of each view's leading dimensions when one of
-    them is not contiguous.  views: (field, name, tensor or None); first: offset of the stride
-    fields, which make() leaves 0 (contiguous)."""
-    plain = not any(memoryview(p).cast("B")[first:])
-    if plain and all(t is None or t.is_contiguous() for _, _, t in views):
-        return p
+def _views(validate, p, dev, first, specs):
+    """Addresses of tensors (name, tensor, shape, dtype, stride field) that may be strided views, and
+    the params with their strides: p itself when all are contiguous (the stride fields begin at
+    byte `first` and are 0 in params from make())."""
+    out, plain = [], ctypes.string_at(ctypes.addressof(p) + first, ctypes.sizeof(p) - first) == _ZEROS[first]
+    for name, t, shape, dt, _ in specs:
+        if t.shape != shape or t.dtype is not dt or t.get_device() != dev:
+            _refuse((validate(p), name), name, t, shape, dt, dev)
+        if plain and not t.is_contiguous():
+            plain = False
+        out.append(t.data_ptr())
+    if plain:
+        return p, out
     q = type(p).from_buffer_copy(p)
-    for field, name, t in views:
-        out = getattr(q, field)
-        for i in range(len(out)):
-            out[i] = 0
-        if t is None or t.is_contiguous():
+    for name, t, _, _, field in specs:
+        st = getattr(q, field)
+        for i in range(len(st)):
+            st[i] = 0
+        if t.is_contiguous():
             continue
         if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
-        for i in range(len(out)):
+        for i in range(len(st)):
             # a dimension of one element has no stride of its own: take a contiguous one
-            out[i] = t.stride(i) if t.shape[i] > 1 else _packed(t, i)
-        if t.numel() and not any(out):     # all zero would mean contiguous to the library
+            st[i] = t.stride(i) if t.shape[i] > 1 else _packed(t, i)
+        if t.numel() and not any(st):     # all zero would mean contiguous to the library
             raise ValueError(f"{name}: one row expanded over every dimension is not supported")
-    return q
+    return q, out
+
+
+_ZEROS = {RopeParams.x_stride.offset: bytes(ctypes.sizeof(RopeParams) - RopeParams.x_stride.offset),
+          CacheParams.q_stride.offset: bytes(ctypes.sizeof(CacheParams) - CacheParams.q_stride.offset)}
 
 
 def _packed(t, d):
@@ -478,27 +492,27 @@ def _packed(t, d):
     return n
 
 
-def _launch(fn, name, dev, *args):
-    """fn(*args, stream) on device dev and its current stream."""
+def _elem(p):
+    dt = _torch().elem.get(p.dtype)
+    if dt is None:
+        raise ValueError(f"unknown dtype code {p.dtype}")
+    return dt
+
+
+def _launch(fn, validate, p, name, dev, *args):
+    """fn(p, *args, stream) on device dev and its current stream."""
     if dev < 0:
+        _check(validate(p), name)
         raise ValueError("tensors must be on a CUDA device")
-    torch = _torch().mod
+    torch = _tc.mod
     stream = torch._C._cuda_getCurrentRawStream(dev)     # current_stream(dev).cuda_stream, without the object
     if torch.cuda.current_device() == dev:
-        status = fn(*args, stream)
+        status = fn(p, *args, stream)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, stream)
+            status = fn(p, *args, stream)
     if status != 0:
         raise SparsePRError(status, name)
-
-
-def _addr(t):
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError("tensor must be contiguous")
-    return t.data_ptr()
 
 
 def sparsepr_rope_validate(p: RopeParams) -> int:
@@ -524,23 +538,20 @@ def rope_frequencies(p: RopeParams, device):
 
 
 def _rope(fn, name, p, x, pos, freq, y, x2, y2):
-    _check(_lib.sparsepr_rope_validate(p), name)
-    if (p.H2 > 0) != (x2 is not None) or (x2 is None) != (y2 is None):
+    H2 = p.H2
+    if (H2 > 0) != (x2 is not None) or (x2 is None) != (y2 is None):
         raise ValueError("the second tensor goes with H2 > 0")
+    check = _lib.sparsepr_rope_validate
     dev, el, B, N, d = x.get_device(), _elem(p), p.B, p.N, p.d
     shape = (B, p.H, N, d)
-    _expect("x", x, shape, el, dev)
-    _expect("y", y, shape, el, dev)
+    specs = [("x", x, shape, el, "x_stride"), ("y", y, shape, el, "y_stride")]
     if x2 is not None:
-        shape = (B, p.H2, N, d)
-        _expect("x2", x2, shape, el, dev)
-        _expect("y2", y2, shape, el, dev)
-    _expect("pos", pos, (p.n_axes, B, N) if p.pos_batched else (p.n_axes, N), _tc.i32, dev)
-    _expect("freq", freq, (p.rot_dim // 2,), _tc.f64, dev)
-    q = _strided(p, RopeParams.x_stride.offset, (("x_stride", "x", x), ("y_stride", "y", y), ("x2_stride", "x2", x2),
-                                                 ("y2_stride", "y2", y2)))
-    _launch(fn, name, dev, q, x.data_ptr(), _addr(pos), _addr(freq), y.data_ptr(),
-            None if x2 is None else x2.data_ptr(), None if y2 is None else y2.data_ptr())
+        shape = (B, H2, N, d)
+        specs += [("x2", x2, shape, el, "x2_stride"), ("y2", y2, shape, el, "y2_stride")]
+    q, v = _views(check, p, dev, RopeParams.x_stride.offset, specs)
+    ps, fr = _pointers(check, p, dev, (("pos", pos, (p.n_axes, B, N) if p.pos_batched else (p.n_axes, N), _tc.i32),
+                                       ("freq", freq, (p.rot_dim // 2,), _tc.f64)))
+    _launch(fn, check, q, name, dev, v[0], ps, fr, v[1], *(v[2:] or (None, None)))
 
 
 def sparsepr_rope(p: RopeParams, x, pos, freq, y, x2=None, y2=None):
@@ -576,7 +587,8 @@ def sparsepr_paged_error(ws) -> int:
 
 
 def sparsepr_paged_clear_error(ws):
-    _launch(_lib.sparsepr_paged_clear_error, "sparsepr_paged_clear_error", ws.get_device(), _addr(ws))
+    with _torch().mod.cuda.device(ws.device):
+        _check(_lib.sparsepr_paged_clear_error(_ptr(ws), _stream(ws)), "sparsepr_paged_clear_error")
 
 
 def sparsepr_select_units(p: CacheParams) -> int:
@@ -606,84 +618,74 @@ def alloc_cache(p: CacheParams, device):
                 k_mean=torch.empty(p.n_pages, p.Hkv, p.d, dtype=dt, device=device))
 
 
-def _sequences(p, dev, q_start, kv_len, page_table, ws):
+def _sequences(p, q_start, kv_len, page_table):
     i32, B = _tc.i32, p.B
-    _expect("q_start", q_start, (B + 1,), i32, dev)
-    _expect("kv_len", kv_len, (B,), i32, dev)
-    _expect("page_table", page_table, (B, p.max_pages), i32, dev)
-    if ws.dtype is not _tc.u8 or ws.get_device() != dev:
-        raise ValueError("ws must be a uint8 tensor on the tensors' device")
+    return [("q_start", q_start, (B + 1,), i32), ("kv_len", kv_len, (B,), i32),
+            ("page_table", page_table, (B, p.max_pages), i32)]
 
 
-def _lists(p, dev, sel, sel_count):
+def _lists(p, sel, sel_count):
     n = _lib.sparsepr_select_units(p)
     if n < 0:
         sparsepr_select_units(p)     # raises
-    _expect("sel", sel, (n, p.Hkv, p.n_select), _tc.i32, dev)
-    _expect("sel_count", sel_count, (n, p.Hkv), _tc.i32, dev)
+    return [("sel", sel, (n, p.Hkv, p.n_select), _tc.i32), ("sel_count", sel_count, (n, p.Hkv), _tc.i32)]
 
 
 def sparsepr_cache_append(p: CacheParams, K, V, q_start, kv_len, page_table, k_pages, v_pages, k_mean, ws, rope=None,
                           pos=None, freq=None):
     """Writes the new rows K, V [T, Hkv, d] into their page slots and the touched pages' mean
     keys; with rope (RopeParams) the keys are rotated by pos int32 [n_axes, T] on the way."""
-    _check(_lib.sparsepr_cache_validate(p), "sparsepr_cache_append")
+    check = _lib.sparsepr_cache_validate
     dev, el, T, Hkv, d = K.get_device(), _elem(p), p.T, p.Hkv, p.d
-    _expect("K", K, (T, Hkv, d), el, dev)
-    _expect("V", V, (T, Hkv, d), el, dev)
-    _sequences(p, dev, q_start, kv_len, page_table, ws)
-    pages = (p.n_pages, Hkv, p.page, d)
-    _expect("k_pages", k_pages, pages, el, dev)
-    _expect("v_pages", v_pages, pages, el, dev)
-    _expect("k_mean", k_mean, (p.n_pages, Hkv, d), el, dev)
+    rows, pages = (T, Hkv, d), (p.n_pages, Hkv, p.page, d)
+    q, (kp, vp) = _views(check, p, dev, CacheParams.q_stride.offset, (("K", K, rows, el, "k_stride"),
+                                                                     ("V", V, rows, el, "v_stride")))
+    specs = _sequences(p, q_start, kv_len, page_table)
+    specs += [("k_pages", k_pages, pages, el), ("v_pages", v_pages, pages, el),
+              ("k_mean", k_mean, (p.n_pages, Hkv, d), el), ("ws", ws, (ws.numel(),), _tc.u8)]
     if rope is not None:
         if pos is None or freq is None:
             raise ValueError("rope needs pos and freq")
-        _expect("pos", pos, (rope.n_axes, T), _tc.i32, dev)
-        _expect("freq", freq, (rope.rot_dim // 2,), _tc.f64, dev)
-    else:
-        pos = freq = None
-    q = _strided(p, CacheParams.q_stride.offset, (("k_stride", "K", K), ("v_stride", "V", V)))
-    _launch(_lib.sparsepr_cache_append, "sparsepr_cache_append", dev, q, K.data_ptr(), V.data_ptr(), _addr(q_start),
-            _addr(kv_len), _addr(page_table), _addr(k_pages), _addr(v_pages), _addr(k_mean), rope, _addr(pos),
-            _addr(freq), _addr(ws), ws.numel())
+        specs += [("pos", pos, (rope.n_axes, T), _tc.i32), ("freq", freq, (rope.rot_dim // 2,), _tc.f64)]
+    t = _pointers(check, p, dev, specs)
+    ps, fr = t[7:] or (None, None)
+    _launch(_lib.sparsepr_cache_append, check, q, "sparsepr_cache_append", dev, kp, vp, *t[:6], rope, ps, fr, t[6],
+            ws.numel())
 
 
 def sparsepr_page_select(p: CacheParams, Q, q_start, kv_len, page_table, k_mean, sel, sel_count, ws):
     """Page lists of every unit of q_block tokens and key/value head, by mean query . mean key."""
-    _check(_lib.sparsepr_cache_validate(p), "sparsepr_page_select")
+    check = _lib.sparsepr_cache_validate
     dev, el = Q.get_device(), _elem(p)
-    _expect("Q", Q, (p.T, p.Hq, p.d), el, dev)
-    _sequences(p, dev, q_start, kv_len, page_table, ws)
-    _expect("k_mean", k_mean, (p.n_pages, p.Hkv, p.d), el, dev)
-    _lists(p, dev, sel, sel_count)
-    q = _strided(p, CacheParams.q_stride.offset, (("q_stride", "Q", Q),))
-    _launch(_lib.sparsepr_page_select, "sparsepr_page_select", dev, q, Q.data_ptr(), _addr(q_start), _addr(kv_len),
-            _addr(page_table), _addr(k_mean), _addr(sel), _addr(sel_count), _addr(ws), ws.numel())
+    q, (qp,) = _views(check, p, dev, CacheParams.q_stride.offset, (("Q", Q, (p.T, p.Hq, p.d), el, "q_stride"),))
+    t = _pointers(check, p, dev, _sequences(p, q_start, kv_len, page_table) +
+                  [("k_mean", k_mean, (p.n_pages, p.Hkv, p.d), el)] + _lists(p, sel, sel_count) +
+                  [("ws", ws, (ws.numel(),), _tc.u8)])
+    _launch(_lib.sparsepr_page_select, check, q, "sparsepr_page_select", dev, qp, *t, ws.numel())
 
 
 def sparsepr_paged_attention(p: CacheParams, Q, q_start, kv_len, page_table, k_pages, v_pages, O, lse, ws, sel=None,
                              sel_count=None):
     """Attention of the new tokens Q [T, Hq, d] over the cache into O (and lse float32 [T, Hq] or
     None); with sel and sel_count over the pages of their lists."""
-    _check(_lib.sparsepr_cache_validate(p), "sparsepr_paged_attention")
-    dev, el, T, Hq, d = Q.get_device(), _elem(p), p.T, p.Hq, p.d
-    _expect("Q", Q, (T, Hq, d), el, dev)
-    _expect("O", O, (T, Hq, d), el, dev)
-    if lse is not None:
-        _expect("lse", lse, (T, Hq), _tc.f32, dev)
-    _sequences(p, dev, q_start, kv_len, page_table, ws)
-    pages = (p.n_pages, p.Hkv, p.page, d)
-    _expect("k_pages", k_pages, pages, el, dev)
-    _expect("v_pages", v_pages, pages, el, dev)
     if (sel is None) != (sel_count is None):
         raise ValueError("sel and sel_count come together")
+    check = _lib.sparsepr_cache_validate
+    dev, el, T, Hq, d = Q.get_device(), _elem(p), p.T, p.Hq, p.d
+    rows, pages = (T, Hq, d), (p.n_pages, p.Hkv, p.page, d)
+    q, (qp, op) = _views(check, p, dev, CacheParams.q_stride.offset, (("Q", Q, rows, el, "q_stride"),
+                                                                     ("O", O, rows, el, "o_stride")))
+    specs = _sequences(p, q_start, kv_len, page_table)
+    specs += [("k_pages", k_pages, pages, el), ("v_pages", v_pages, pages, el), ("ws", ws, (ws.numel(),), _tc.u8)]
+    if lse is not None:
+        specs.append(("lse", lse, (T, Hq), _tc.f32))
     if sel is not None:
-        _lists(p, dev, sel, sel_count)
-    q = _strided(p, CacheParams.q_stride.offset, (("q_stride", "Q", Q), ("o_stride", "O", O)))
-    _launch(_lib.sparsepr_paged_attention, "sparsepr_paged_attention", dev, q, Q.data_ptr(), _addr(q_start),
-            _addr(kv_len), _addr(page_table), _addr(k_pages), _addr(v_pages), _addr(sel), _addr(sel_count),
-            O.data_ptr(), _addr(lse), _addr(ws), ws.numel())
+        specs += _lists(p, sel, sel_count)
+    t = _pointers(check, p, dev, specs)
+    z = t.pop(6) if lse is not None else None
+    sp, cp = t[6:] or (None, None)
+    _launch(_lib.sparsepr_paged_attention, check, q, "sparsepr_paged_attention", dev, qp, *t[:5], sp, cp, op, z, t[5],
+            ws.numel())
 
 
 def rollout_step(p: CacheParams, cache, Q, K, V, q_start, kv_len, page_table, O, ws, rope=None, pos=None, freq=None,
