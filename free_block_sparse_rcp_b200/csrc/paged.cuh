@@ -220,7 +220,8 @@ __device__ __forceinline__ int visible_end(int pos, int frame, int len) {
 __device__ __forceinline__ int stream_limit(int end, const int* __restrict__ list, int cnt, int page,
                                            int* entries = nullptr) {
   if (!list) return end;
-  int lo = 0, hi = cnt;            // entries whose page starts below `end`
+  int lo = 0, hi = cnt;            // entries whose page starts below `end`: mostly all
+  if (cnt > 0 && (long long)list[cnt - 1] * page < end) lo = cnt;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if ((long long)list[mid] * page < end) lo = mid + 1; else hi = mid;

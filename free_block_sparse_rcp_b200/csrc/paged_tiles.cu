@@ -7,8 +7,7 @@
 //   warps 0-7, 8-15  softmax and epilogue of tile 0 and 1: two threads per query row r = TMEM lane r,
 //                    each with 32 of every 64 keys (a single warp per scheduler and tile stalls on
 //                    its own exponentials: 13 cycles per element against 8.4 with two)
-//   warp 16          TMA: boxes of min(page, 128) rows of the pages of a chunk (K ring of 3, V
-//                    ring of 2)
+//   warp 16          TMA: boxes of min(page, 128) rows of the pages of a chunk, into rings of K and V
 //   warp 17          issues the MMAs
 //   warps 18-19      walk the CTA's work list and load the query rows
 // TMEM (512 columns): S, O and P of both tiles, P as packed 16-bit pairs and the second product's A
@@ -39,7 +38,7 @@ namespace paged {
 
 using namespace spr::tc;
 
-constexpr int BM = 128, TPC = 2, BN = kPagedTileBN, KST = 3, VST = 2;
+constexpr int BM = 128, TPC = 2, BN = kPagedTileBN;
 constexpr int PROD_WARP = 16, MMA_WARP = 17, LOAD_WARP = 18, NTT = 640;
 constexpr int NSOFT = 256;             // softmax threads of a tile
 constexpr uint32_t kCols = 512;
@@ -56,8 +55,15 @@ struct Seg {
   const int* list;
 };
 
+// K and V chunks in shared memory: as many as fit with d = 128, five of each with d = 64
+template <int D>
+struct Ring {
+  static constexpr int K = D == 64 ? 5 : 3, V = D == 64 ? 5 : 2;
+};
+constexpr int kMaxRing = 5;
+
 struct TileBars {
-  uint64_t q, qfree, kfull[KST], kempty[KST], vfull[VST], vempty[VST], vtail, s_full[TPC], p_full[TPC][2], pv_half[TPC],
+  uint64_t q, qfree, kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing], vtail, s_full[TPC], p_full[TPC][2], pv_half[TPC],
       pv_done[TPC], s_free[TPC], o_done[TPC], o_free[TPC], seg_full[2], seg_free[2], mma_done;
 };
 
@@ -66,14 +72,14 @@ struct TileLayout {
   static constexpr uint32_t kTile = (uint32_t)D * 128 * 2;
   static constexpr uint32_t oQ = 0;
   static constexpr uint32_t oK = oQ + TPC * kTile;
-  static constexpr uint32_t oV = oK + KST * kTile;
-  static constexpr uint32_t oBar = oV + VST * kTile;
-  static constexpr uint32_t oSeg = oBar + 320;
+  static constexpr uint32_t oV = oK + Ring<D>::K * kTile;
+  static constexpr uint32_t oBar = oV + Ring<D>::V * kTile;
+  static constexpr uint32_t oSeg = oBar + 384;
   static constexpr uint32_t oInt = oSeg + 256;
   static constexpr uint32_t oEx = oInt + 64;                 // [tile][half][row] exchange of the row's threads
   static constexpr uint32_t kBytes = oEx + TPC * 2 * BM * 4;
 };
-static_assert(sizeof(TileBars) <= 320 && 2 * sizeof(Seg) <= 256, "barrier and segment blocks");
+static_assert(sizeof(TileBars) <= 384 && 2 * sizeof(Seg) <= 256, "barrier and segment blocks");
 
 // Taking up an entry (its rows, the first softmax, the epilogue) costs about as much as two chunks:
 // an entry's cost begins with that many.
@@ -296,6 +302,7 @@ template <typename T, int D, bool SEL>
 __global__ void __launch_bounds__(NTT, 1)
     k_paged_tiles(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, Args a) {
   using L = TileLayout<D>;
+  constexpr int KST = Ring<D>::K, VST = Ring<D>::V;
   constexpr float SHIFT = ProbShift<T>::v;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = su32(smem);
@@ -623,6 +630,7 @@ __global__ void __launch_bounds__(NTT, 1)
     const int pair = 1 + t * 4 + (warp & 3);           // named barrier of the two warps of these rows
     float* mine = reinterpret_cast<float*>(smem + L::oEx) + (t * 2 + hv) * BM + r;
     const float* other = reinterpret_cast<const float*>(smem + L::oEx) + (t * 2 + (hv ^ 1)) * BM + r;
+    const bool wide_rows = (((uintptr_t)a.O | (uintptr_t)(a.ost * 2) | (uintptr_t)(a.osh * 2)) & 31) == 0;
     bool ok = true;
     int tc = 0, use = 0;              // chunks and segments of this tile so far
     Seg g;
@@ -780,14 +788,22 @@ __global__ void __launch_bounds__(NTT, 1)
                   make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
                               __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+            // a lane's row is its own: 32 bytes per store fill whole sectors where the rows allow it
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
+            for (int e = 0; e < 2; ++e) {
+              uint32_t w[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack2<T>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 8; ++k)
+                w[k] = pack2<T>(__uint_as_float(o[16 * e + 2 * k]) * inv, __uint_as_float(o[16 * e + 2 * k + 1]) * inv);
+              T* dst = orow + c * 32 + e * 16;
+              if (wide_rows) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                             "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                             : "memory");
+              } else {
+                reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
             }
           }
         }
