@@ -70,13 +70,14 @@ struct ProbShift<__half> {
   static constexpr float v = 7.f;
 };
 
-// Largest sum of a half chunk's probabilities against an earlier maximum: below fp16's largest
-// value; bf16 and the fp32 sums only need room below 2^128.
+// Largest sum of a thread's probabilities of a step against an earlier maximum, before the sums are
+// rescaled: below fp16's largest value, and for bf16 far enough from fp32's that sums with values
+// of 10^30 hold.
 template <typename T>
 struct ProbBound;
 template <>
 struct ProbBound<__nv_bfloat16> {
-  static constexpr float v = 18446744073709551616.f;   // 2^64
+  static constexpr float v = 1048576.f;   // 2^20
 };
 template <>
 struct ProbBound<__half> {

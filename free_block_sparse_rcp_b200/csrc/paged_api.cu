@@ -203,7 +203,7 @@ PagedPlan plan_of(const sparsepr_cache_params& p, bool sel) {
 }
 
 int select_units(const sparsepr_cache_params& p) {
-  const long long u = (long long)p.T / p.q_block + p.B;
+  const long long u = ((long long)p.T + (p.q_block - 1ll) * p.B) / p.q_block;   // sum of ceil(n / q_block)
   return (int)(u < p.T ? u : p.T);
 }
 

@@ -94,7 +94,8 @@ __device__ __forceinline__ bool load_item(const Args& a, int idx, int h, int* sm
   const int end = visible_end(it.s.len - it.s.n + it.tok0 + it.ntok - 1, a.frame, it.s.len);
   int seen = it.cnt;
   it.total = stream_limit(end, it.list, it.cnt, a.page, &seen);
-  it.bad |= seen != it.cnt;      // the unit's last token sees every page of its list
+  // the unit's last token sees every page of its list, and no page is there twice
+  it.bad |= seen != it.cnt || it.total > end;
   return true;
 }
 
@@ -506,7 +507,7 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int
   p.rows = rows <= 32;
   p.mt = rows <= 16 ? 1 : 2;
   p.ppu = 1;
-  const long long units = sel ? (long long)T / q_block + B : B;
+  const long long units = sel ? ((long long)T + (q_block - 1ll) * B) / q_block : B;   // sum of ceil(n / q_block)
   long long items = units < T || !sel ? units : T;
   if (p.rows) {
     p.kind = sel ? paged::kUnits : paged::kWhole;

@@ -265,9 +265,10 @@ __device__ __forceinline__ void make_seg(const Args& a, long long e, int n_items
     const int c = a.sel_cnt[at];
     g.cnt = min(max(c, 0), a.n_select);
     const int ul = g.tok0 + min(a.q_block, s.n - g.tok0) - 1;     // the unit's last token sees every page of the list
+    const int end = visible_end(s.len - s.n + ul, a.frame, s.len);
     int seen = g.cnt;
-    stream_limit(visible_end(s.len - s.n + ul, a.frame, s.len), g.list, g.cnt, a.page, &seen);
-    if (c != g.cnt || seen != g.cnt) g.bad = 1;
+    // (more keys than there are: a page twice, perhaps behind the chunks that the plan counted)
+    if (stream_limit(end, g.list, g.cnt, a.page, &seen) > end || c != g.cnt || seen != g.cnt) g.bad = 1;
   }
   auto limit_of = [&](int r) -> int {
     return stream_limit(visible_end(s.len - s.n + g.tok0 + (g.row0 + r) / a.G, a.frame, s.len), g.list, g.cnt, a.page);
@@ -634,7 +635,11 @@ __global__ void __launch_bounds__(NTT, 1)
     bool ok = true;
     int tc = 0, use = 0;              // chunks and segments of this tile so far
     Seg g;
-    for (int i = 0; ok && get_seg(i, g); ++i) {
+    for (int i = 0;; ++i) {
+      // after a timeout the two warps of a row's threads may see different answers: they leave
+      // together, or one would wait at their barrier for ever
+      const bool got = ok && get_seg(i, g);
+      if (!bar_and(pair, 64, got)) break;
       const int ntile = g.nrows > BM ? 2 : 1;
       const bool in = row < g.nrows;
       const int nct = t < ntile ? (t == 0 ? g.nch0 : g.nch) : 0;

@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
   if (!live || b < 0 || b >= a.B || row < a.q_start[b]) return;
   const int qs = a.q_start[b], qe = a.q_start[b + 1], lenr = a.kv_len[b];
   const int n = qe - qs, len = min(max(lenr, 0), a.max_pages * page);
-  if (u == 0 && row == qs && blockIdx.y == 0 && (qs < 0 || qe > a.T || len != lenr || n > a.max_chunk))
+  if (u == 0 && row == max(qs, 0) && blockIdx.y == 0 && (qs < 0 || qe > a.T || len != lenr || n > a.max_chunk))
     set_error(a.err, DERR_INDEX);
   const int slot = len - n + (row - qs);
   if (slot < 0 || slot >= len) return;

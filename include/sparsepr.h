@@ -323,7 +323,8 @@ SPARSEPR_API sparsepr_status sparsepr_workspace_clear_error(const sparsepr_param
  * sparsepr_paged_workspace_bytes() with its own error query, sparsepr_paged_error().
  * The entry points of this section never clear the error word except for
  * sparsepr_paged_clear_error(): clear it once after allocating the workspace.  Calls that
- * may overlap on the GPU need a workspace each.                                        */
+ * may overlap on the GPU need a workspace each.  All calls can be captured into CUDA graphs;
+ * a graph's calls keep the workspace they were captured with.                                        */
 
 /* element types */
 #define SPARSEPR_BF16 0
@@ -439,12 +440,14 @@ SPARSEPR_API sparsepr_status sparsepr_cache_append(const sparsepr_cache_params* 
 
 /* Lists of pages for sparsepr_paged_attention.  A unit is q_block consecutive new tokens of
  * one sequence (the last one may be shorter); units are numbered sequence by sequence, and
- * there are at most sparsepr_select_units(p) = T / q_block + B of them (min T).  For a unit
+ * there are at most sparsepr_select_units(p) = (T + (q_block - 1) B) / q_block of them (min T).
+ * For a unit
  * and key/value head the score of a page is (mean of the unit's query rows over its tokens
  * and the query heads of that key/value head) . k_mean[page], summed in 64 bits.  The pages
  * that hold a key visible to the unit's last token take part; the first n_sink and the last
  * n_recent of them are kept, and the best scores fill the list up to n_select (ties to the
- * lowest page, NaN counts as the lowest score).
+ * lowest page; a page whose mean, or a unit whose mean query, has an element that is not finite
+ * has no score and counts as the lowest).
  *   sel       int32 [units, Hkv, n_select]  page indices within the sequence, ascending, -1 behind
  *   sel_count int32 [units, Hkv]            entries of each list
  * Rows of units that do not exist are left as they were.  A page id out of [0, n_pages) is
@@ -458,13 +461,14 @@ SPARSEPR_API sparsepr_status sparsepr_page_select(const sparsepr_cache_params* p
 /* Attention of the new tokens over the cache:
  *   O(i, h) = sum over visible keys j of softmax_j(s q.k_j) v_j,  lse(i, h) = ln sum exp(s q.k_j)
  * (O [T, Hq, d]; lse float [T, Hq], may be NULL), over the pages of the token's list when sel
- * and sel_count are given (n_select > 0), else over the whole cache.  A token that sees no
- * key gets O = 0 and lse = -inf.  Keys past kv_len, and keys that no token of a block of
+ * and sel_count are given (n_select > 0), else over the whole cache.  O must not overlap Q.  A
+ * token that sees no key gets O = 0 and lse = -inf.  Keys past kv_len, and keys that no token of a block of
  * rows sees, are never used, whatever their slots hold (a NaN or an infinity in a value row
  * that some tokens of a block see can reach the block's other rows).
  * A page id out of [0, n_pages), a list that is not strictly ascending or leaves the visible
- * pages, or a kv_len out of [0, max_pages * page] is device error 1; the rows that depend on
- * it become NaN.                                                                        */
+ * pages, a kv_len out of [0, max_pages * page] or a sequence of more than max_chunk new tokens
+ * is device error 1; the rows that depend on it become NaN (of such a sequence, those that are
+ * written).                                                                        */
 SPARSEPR_API sparsepr_status sparsepr_paged_attention(const sparsepr_cache_params* p, const void* Q,
                                                       const int* q_start, const int* kv_len,
                                                       const int* page_table, const void* k_pages,

@@ -310,6 +310,27 @@ def test_attention_many_small_weights_fp16(spr, gpu, new, kv):
     s.check(*s.attend())
 
 
+def test_a_list_longer_than_the_cache_is_an_error(spr, gpu):
+    """Every page once and the last one again, behind the chunks that the visible keys need."""
+    s = Scene(spr, gpu, [40], [1280], Hq=2, Hkv=1, d=64, page=128, dt=BF, frame=0, q_block=40, n_select=12, seed=25)
+    sel = torch.tensor([[list(range(10)) + [9, 9]]], dtype=torch.int32, device=gpu)
+    O, _ = s.attend(sel, torch.full((1, 1), 12, dtype=torch.int32, device=gpu))
+    assert spr.sparsepr_paged_error(s.ws) == 1 and torch.isnan(O).all()
+
+
+@pytest.mark.parametrize("new,kv,d", [([2], [700], 64), ([50], [700], 64), ([50], [700], 128)])
+def test_attention_large_values(spr, gpu, new, kv, d):
+    """Values of 10^30 with a maximum that grows by thirty powers of two along the keys."""
+    s = Scene(spr, gpu, new, kv, Hq=2, Hkv=1, d=d, page=32, dt=BF, frame=0, seed=35)
+    s.Q.fill_(0)
+    s.Q[:, :, 0] = 8.0
+    for j in range(22):
+        s.kp[int(s.table[0, j]), :, :, 0] = j * 30 * math.log(2) / 21 * math.sqrt(d) / 8
+    s.vp *= 1e30
+    s.dev["kp"], s.dev["vp"], s.dev["Q"] = s.kp.to(gpu), s.vp.to(gpu), s.Q.to(gpu)
+    s.check(*s.attend())
+
+
 @pytest.mark.parametrize("new,kv", [([1, 1], [300, 70]), ([90], [400])])
 def test_attention_strided(spr, gpu, new, kv):
     """Q and O as views of head-major and fused tensors."""
@@ -627,7 +648,7 @@ def test_select_many_pages(spr, gpu, Hkv):
 
 def test_bad_lists_are_errors(spr, gpu):
     for new in ([1, 1], [40, 40]):
-        for what in ("order", "range", "count", "negative"):
+        for what in ("order", "range", "count", "negative", "twice"):
             s = Scene(spr, gpu, new, [300, 300], Hq=2, Hkv=1, d=64, page=16, dt=BF, q_block=40, n_select=6, n_recent=1, seed=25)
             sel, cnt = s.select()
             good, _ = s.attend(sel, cnt)
@@ -637,6 +658,8 @@ def test_bad_lists_are_errors(spr, gpu):
                 sel[1, 0, 5] = 19
             if what == "negative":
                 sel[1, 0, 0] = -1
+            if what == "twice":
+                sel[1, 0, 4] = sel[1, 0, 5].item()
             if what == "count":
                 cnt[1, 0] = 7
             O, _ = s.attend(sel, cnt)

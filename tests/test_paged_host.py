@@ -225,3 +225,46 @@ def test_binding_refuses_wrong_tensors(spr):
         spr.sparsepr_rope(spr.RopeParams.make(1, 2, 3, 64, layout=5), x, pos, f, x)
     with pytest.raises(spr.SparsePRError):
         spr.paged_workspace(_cache(spr, page=8), "cpu")
+
+
+class _FakeCuda:
+    """Stands in for torch where a call picks its device and stream."""
+
+    def __init__(self, current):
+        self.current, self.entered = current, []
+        self.cuda, self._C = self, self
+
+    def current_device(self):
+        return self.current
+
+    def _cuda_getCurrentRawStream(self, dev):
+        return 1000 + dev
+
+    def device(self, dev):
+        fake = self
+
+        class Ctx:
+            def __enter__(self):
+                fake.entered.append(dev)
+
+            def __exit__(self, *a):
+                fake.entered.append(-1)
+        return Ctx()
+
+
+@pytest.mark.parametrize("current,dev", [(0, 0), (0, 1), (1, 0)])
+def test_launches_go_to_the_tensors_device(spr, monkeypatch, current, dev):
+    """A call on tensors of another device than the current one runs there, on that device's
+    current stream, and leaves the current device as it was."""
+    fake = _FakeCuda(current)
+    monkeypatch.setattr(spr._torch(), "mod", fake)
+    seen = []
+
+    def fn(*args):
+        seen.append((args, list(fake.entered)))
+        return 0
+    spr._launch(fn, lambda p: 0, "params", "name", dev, 7, 8)
+    assert seen == [(("params", 7, 8, 1000 + dev), [] if dev == current else [dev])]
+    assert fake.entered == ([] if dev == current else [dev, -1])
+    with pytest.raises(spr.SparsePRError):
+        spr._launch(lambda *a: 4, lambda p: 0, "params", "name", dev)
