@@ -96,7 +96,7 @@ struct Args {
   const int* sel_cnt;
   void* O;
   float* lse;
-  float* part_o;         // rows kernel [S][T * Hq][d], tile kernel [2 kPlanCtas][256][d]
+  float* part_o;         // rows kernel [slot][16 mt][d], tile kernel [2 kPlanCtas][d / 4][256][4]
   float* part_lse;
   void* plan;            // tile kernel: PlanHead
   int* plan_seq;         // [B + 1] first item of each sequence
@@ -107,7 +107,8 @@ struct Args {
   int q_block, n_select;
   int ppu;               // row parts per unit (selection, tensor-tile kernel), else 1
   int items;             // upper bound of the (sequence, unit, part) items of a head
-  int S, min_split;      // most splits of an item's key stream, fewest tiles of a split
+  int S, min_split;      // rows kernel: pieces to aim for (whole sequences) or pieces of a list at most;
+                         // fewest tiles of a piece
   float scale_log2;
   long long qst, qsh, ost, osh;
 };

@@ -216,11 +216,13 @@ Layout layout_of(const sparsepr_cache_params& p) {
   Layout L{};
   size_t o = 256;   // error word
   auto take = [&](size_t bytes) { const size_t at = o; o = al256(o + bytes); return at; };
-  // partial results: rows of every split (rows kernel), or two pieces per CTA (tile kernel)
+  // partial results: the pieces of cut items (rows kernel), or two pieces per CTA (tile kernel)
   size_t rows = 0, items = 0;
   for (int sel = 0; sel <= (p.n_select > 0 ? 1 : 0); ++sel) {
     const PagedPlan pl = plan_of(p, sel != 0);
-    size_t r = pl.rows ? (pl.S > 1 ? (size_t)pl.S * p.T * p.Hq : 0) : 2ull * kPlanCtas * kPagedTileRows;
+    size_t r = 2ull * kPlanCtas * kPagedTileRows;
+    if (pl.rows && pl.kind == paged::kUnits) r = pl.S > 1 ? (size_t)pl.items * p.Hkv * pl.S * 16 * pl.mt : 0;
+    if (pl.rows && pl.kind == paged::kWhole) r = (size_t)pl.S * 16 * pl.mt;
     rows = r > rows ? r : rows;
     if (!pl.rows && (size_t)pl.items > items) items = pl.items;
   }

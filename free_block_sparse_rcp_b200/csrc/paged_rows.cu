@@ -10,8 +10,10 @@
 //   4 MT warps      warp (mt, slice) takes 16 query rows and 16 of the stage's 64 keys, keeps
 //                   its own running maximum, sum and O in registers; the four slices are joined
 //                   at the end through shared memory
-// Long streams are cut into splits (grid z); a split writes its normalised O and lse in fp32,
-// and k_paged_combine joins them.
+// Whole sequences are cut into pieces of about equal length, so that all of them together fill the
+// GPU once whatever the lengths (find_piece); page lists, which are equally long, into a fixed
+// number.  A piece of a cut item writes its normalised O and lse in fp32, and k_paged_combine joins
+// them.
 #include <cuda.h>
 
 #include "kernels.h"
@@ -64,39 +66,176 @@ __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
 // What an item reads, computed alike by the attention and the join.
 struct Item {
   Seq s;
+  int h;                   // key/value head
   int tok0, ntok;          // tokens of the sequence in this item
   const int* list;         // page list (NULL: the whole cache)
   int cnt, total;          // list entries; keys of the stream
+  int ns, part, slot;      // pieces of the item, this piece, first piece's slot of partial results
   bool bad;
 };
 
-template <int KIND, int NT>
-__device__ __forceinline__ bool load_item(const Args& a, int idx, int h, int* sm, Item& it) {
-  const Found f = find_item<KIND, NT>(a, idx, 0, 1, sm);
+// Pieces of whole sequences.  Of `target` pieces, sequence b with t_b tiles of keys per head gets
+// floor(target t_b / sum t Hkv) per head, at least one and none of fewer than min_split tiles: no
+// more than target pieces are of cut items, which is what the partial results have slots for, and
+// pieces are about equally long however unequal the sequences are.  Every block computes this from
+// q_start and kv_len.  By piece (JOIN false): the idx-th piece; by item (JOIN true): the idx-th cut
+// item.  ns = 0: there is none.
+struct Piece {
+  int b, h, part, ns, slot, lo, hi, len;
+};
+template <int NT, bool JOIN>
+__device__ __forceinline__ Piece find_piece(const Args& a, int idx, int* sm /* [3 NT / 32 + 8] */) {
+  constexpr int NW = NT / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (a.B + NT - 1) / NT;
+  const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+  auto tiles_of = [&](int b, int& lo, int& hi, int& len) -> int {    // -1: no new tokens
+    lo = a.q_start[b];
+    hi = a.q_start[b + 1];
+    len = a.kv_len[b];
+    const Seq s = make_seq(a, b, lo, hi, len);
+    if (s.n <= 0) return -1;
+    return (visible_end(s.len - 1, a.frame, s.len) + BNR - 1) / BNR;
+  };
+  int lo = 0, hi = 0, len = 0, t = -1;
+  if (a.B == 1) {        // nothing to count
+    t = tiles_of(0, lo, hi, len);
+    int ns = t < 0 ? 0 : max(1, min(t / a.min_split, a.S / a.Hkv));
+    if (JOIN && ns <= 1) ns = 0;
+    if (idx >= a.Hkv * (JOIN ? 1 : ns)) ns = 0;
+    const int h = ns == 0 ? 0 : (JOIN ? idx : idx / ns);
+    return Piece{0, h, ns == 0 || JOIN ? 0 : idx - h * ns, ns, h * ns, lo, hi, len};
+  }
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    t = tiles_of(b, lo, hi, len);
+    mine += max(t, 0);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  long long* sums = reinterpret_cast<long long*>(sm);
+  if (lane == 0) sums[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) total += sums[w];
+  total *= a.Hkv;
+  auto pieces_of = [&](int t) -> int {
+    if (t < 2 * a.min_split) return t < 0 ? 0 : 1;
+    const long long n = (long long)t * a.S / total;
+    return n < 1 ? 1 : (int)(n < t / a.min_split ? n : t / a.min_split);
+  };
+  __syncthreads();
+  // pieces, and pieces (by piece) or number (JOIN) of cut sequences before this thread's run
+  int np = 0, nc = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (run > 1) t = tiles_of(b, lo, hi, len);
+    const int ns = pieces_of(t);
+    np += JOIN ? (ns > 1) : ns;
+    nc += ns > 1 ? ns : 0;
+  }
+  int ip = np, ic = nc;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, ip, o), v = __shfl_up_sync(0xffffffffu, ic, o);
+    if (lane >= o) {
+      ip += u;
+      ic += v;
+    }
+  }
+  int* wp = sm;
+  int* wc = sm + NW;
+  int* f = sm + 2 * NW;
+  if (lane == 31) {
+    wp[warp] = ip;
+    wc[warp] = ic;
+  }
+  if (tid == 0) f[1] = 0;
+  __syncthreads();
+  int ap = ip - np, ac = ic - nc;
+#pragma unroll
+  for (int w = 0; w < NW; ++w)
+    if (w < warp) {
+      ap += wp[w];
+      ac += wc[w];
+    }
+  const long long at = (long long)idx;
+  if (at >= (long long)ap * a.Hkv && at < (long long)(ap + np) * a.Hkv) {
+    for (int b = b0; b < b1; ++b) {
+      if (run > 1) t = tiles_of(b, lo, hi, len);
+      const int ns = pieces_of(t);
+      const int c = JOIN ? (ns > 1) : ns;
+      if (at < (long long)(ap + c) * a.Hkv) {
+        f[0] = b;
+        f[1] = ns;
+        f[2] = (int)(at - (long long)ap * a.Hkv);
+        f[3] = ac * a.Hkv;
+        f[4] = lo;
+        f[5] = hi;
+        f[6] = len;
+        break;
+      }
+      ap += c;
+      ac += ns > 1 ? ns : 0;
+    }
+  }
+  __syncthreads();
+  Piece p;
+  p.b = f[0];
+  p.ns = f[1];
+  if (p.ns == 0) return p;
+  const int local = f[2];
+  p.h = JOIN ? local : local / p.ns;
+  p.part = JOIN ? 0 : local - p.h * p.ns;
+  p.slot = f[3] + p.h * p.ns;
+  p.lo = f[4];
+  p.hi = f[5];
+  p.len = f[6];
+  return p;
+}
+
+// kWhole: block x is a piece (or, JOIN, a cut item); kUnits: block (x, y, z) is piece z of the list
+// of unit x and head y.  False: nothing to do.
+template <int KIND, int NT, bool JOIN>
+__device__ __forceinline__ bool load_item(const Args& a, int* sm /* [3 NT / 32 + 8] */, Item& it) {
+  it.list = nullptr;
+  it.cnt = 0;
+  if (KIND == kWhole) {
+    const Piece p = find_piece<NT, JOIN>(a, blockIdx.x, sm);
+    if (p.ns == 0) return false;
+    it.s = make_seq(a, p.b, p.lo, p.hi, p.len);
+    it.bad = it.s.bad;
+    it.h = p.h;
+    it.tok0 = 0;
+    it.ntok = it.s.n;
+    it.ns = p.ns;
+    it.part = p.part;
+    it.slot = p.slot;
+    it.total = visible_end(it.s.len - 1, a.frame, it.s.len);
+    return true;
+  }
+  const Found f = find_item<KIND, NT>(a, blockIdx.x, 0, 1, sm);
   if (f.b < 0) return false;
   it.s = make_seq(a, f.b, f.lo, f.hi, f.len);
   it.bad = it.s.bad;
-  it.list = nullptr;
-  it.cnt = 0;
-  if (KIND == kUnits) {
-    it.tok0 = f.rank * a.q_block;
-    it.ntok = min(a.q_block, it.s.n - it.tok0);
-    const size_t at = (size_t)idx * a.Hkv + h;
-    it.list = a.sel + at * a.n_select;
-    const int c = a.sel_cnt[at];
-    it.cnt = min(max(c, 0), a.n_select);
-    it.bad |= c != it.cnt;
-  } else {
-    it.tok0 = 0;
-    it.ntok = it.s.n;
-  }
+  it.h = blockIdx.y;
+  it.tok0 = f.rank * a.q_block;
+  it.ntok = min(a.q_block, it.s.n - it.tok0);
+  const size_t at = (size_t)blockIdx.x * a.Hkv + it.h;
+  it.list = a.sel + at * a.n_select;
+  const int c = a.sel_cnt[at];
+  it.cnt = min(max(c, 0), a.n_select);
+  it.bad |= c != it.cnt;
   if (it.ntok <= 0) return false;
   const int end = visible_end(it.s.len - it.s.n + it.tok0 + it.ntok - 1, a.frame, it.s.len);
   int seen = it.cnt;
   it.total = stream_limit(end, it.list, it.cnt, a.page, &seen);
   // the unit's last token sees every page of its list, and no page is there twice
   it.bad |= seen != it.cnt || it.total > end;
-  return true;
+  it.ns = split_count((it.total + BNR - 1) / BNR, a.S, a.min_split);
+  it.part = JOIN ? 0 : blockIdx.z;
+  it.slot = (int)(at * a.S);
+  return JOIN ? it.ns > 1 : it.part < it.ns;
 }
 
 // Page of stream row p (a multiple of the box height), checked: -1 if it may not be read.
@@ -120,10 +259,10 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
   constexpr float SHIFT = ProbShift<T>::v;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint64_t s_full[ST], s_empty[ST];
-  __shared__ int s_abort, s_bad, s_find[NT / 32 + 8];
+  __shared__ __align__(8) int s_find[3 * NT / 32 + 8];
+  __shared__ int s_abort, s_bad;
   __shared__ float s_m[MT][4][16], s_l[MT][4][16];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int idx = blockIdx.x, h = blockIdx.y;
   const uint32_t base = su32(smem);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");     // the join may get ready
   if (tid < 2) prefetch_tmap(tid ? &tmv : &tmk);
@@ -132,11 +271,9 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
     return;
   }
   Item it;
-  if (!load_item<KIND, NT>(a, idx, h, s_find, it)) return;
-  const int tiles = (it.total + BNR - 1) / BNR;
-  const int ns = split_count(tiles, a.S, a.min_split);
-  if ((int)blockIdx.z >= ns) return;
-  const int t0 = split_at(tiles, blockIdx.z, ns), t1 = split_at(tiles, blockIdx.z + 1, ns);
+  if (!load_item<KIND, NT, false>(a, s_find, it)) return;
+  const int tiles = (it.total + BNR - 1) / BNR, ns = it.ns, h = it.h;
+  const int t0 = split_at(tiles, it.part, ns), t1 = split_at(tiles, it.part + 1, ns);
   if (tid == 0) {
     s_abort = 0;
     s_bad = it.bad ? 1 : 0;
@@ -369,7 +506,7 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
       const int tok = row / a.G, gh = row - tok * a.G;
       const long long qrow = it.s.q0 + it.tok0 + tok;
       const int qh = h * a.G + gh;
-      const size_t prow = ((size_t)blockIdx.z * a.T + qrow) * a.Hq + qh;
+      const size_t prow = (size_t)(it.slot + it.part) * (16 * MT) + row;      // [slot][16 MT rows]
       T* op = (T*)a.O + qrow * a.ost + (long long)qh * a.osh;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -387,25 +524,24 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
 }
 
 // ---------------------------------------------------------------------------
-// Join of split items: grid (items, Hkv), rows of the item dealt to the block's warps.
+// Join of cut items: a block per cut item (kWhole) or per unit and head (kUnits), rows of the item
+// dealt to the block's warps.
 //   O = sum_s exp(lse_s - lse) O_s,  lse = ln sum_s exp(lse_s)
 // ---------------------------------------------------------------------------
 constexpr int kCombThreads = 256;
 
 template <typename T, int D, int KIND>
 __global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int max_rows) {
-  __shared__ int s_find[kCombThreads / 32 + 8];
-  const int idx = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ __align__(8) int s_find[3 * kCombThreads / 32 + 8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Item it;
-  const bool any = load_item<KIND, kCombThreads>(a, idx, h, s_find, it);
+  const bool any = load_item<KIND, kCombThreads, true>(a, s_find, it);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the parts are complete
   if (!any) return;
-  const int nrows = min(it.ntok * a.G, max_rows);
-  const int ns = split_count((it.total + BNR - 1) / BNR, a.S, a.min_split);
-  if (ns <= 1) return;
+  const int nrows = min(it.ntok * a.G, max_rows), ns = it.ns, h = it.h;
   for (int r = warp; r < nrows; r += kCombThreads / 32) {
     const int tok = r / a.G, qh = h * a.G + (r - tok * a.G);
-    const size_t qrow = (size_t)it.s.q0 + it.tok0 + tok, prow = qrow * a.Hq + qh, step = (size_t)a.T * a.Hq;
+    const size_t qrow = (size_t)it.s.q0 + it.tok0 + tok, prow = (size_t)it.slot * max_rows + r, step = max_rows;
     const float* po = a.part_o + prow * D + lane * (D / 32);
     constexpr int UN = 16;              // parts in flight; the first ones beside their lse
     float v[UN][D / 32];
@@ -428,30 +564,29 @@ __global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int max_
       }
     };
     load(0);
-    // lane s holds the lse of the parts s and s + 32 (S <= 64)
-    float z[2], mx = -INFINITY;
+    // the largest lse of all parts; the weights and their sum come with the parts
+    float mx = -INFINITY;
     bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      z[i] = lane + 32 * i < ns ? a.part_lse[prow + (lane + 32 * i) * step] : -INFINITY;
-      nan |= !(z[i] == z[i]);
-      mx = fmaxf(mx, z[i]);
+    for (int s = lane; s < ns; s += 32) {
+      const float z = a.part_lse[prow + s * step];
+      nan |= !(z == z);
+      mx = fmaxf(mx, z);
     }
     mx = warp_max(mx);
     nan = __any_sync(0xffffffffu, nan);
     const float mu = mx == -INFINITY ? 0.f : mx;
-    const float w[2] = {expf(z[0] - mu), expf(z[1] - mu)};
-    float den = warp_sum(w[0] + w[1]);
+    float den = 0.f;
     float acc[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
     for (int s0 = 0; s0 < ns; s0 += UN) {
       if (s0 > 0) load(s0);
+      const float w = lane < UN && s0 + lane < ns ? expf(a.part_lse[prow + (s0 + lane) * step] - mu) : 0.f;
+      den += warp_sum(w);
 #pragma unroll
       for (int i = 0; i < UN; ++i) {
-        const int s = s0 + i;
-        const float ws = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
-        if (s >= ns) continue;
+        const float ws = __shfl_sync(0xffffffffu, w, i);
+        if (s0 + i >= ns) continue;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) acc[k] += ws * v[i][k];
       }
@@ -462,7 +597,7 @@ __global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int max_
 #pragma unroll
     for (int i = 0; i < D / 32; i += 2)
       *reinterpret_cast<uint32_t*>(op + i) = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[prow] = nan ? __int_as_float(0x7fffffff) : (den > 0.f ? mu + logf(den) : -INFINITY);
+    if (lane == 0 && a.lse) a.lse[qrow * a.Hq + qh] = nan ? __int_as_float(0x7fffffff) : (den > 0.f ? mu + logf(den) : -INFINITY);
   }
 }
 
@@ -476,7 +611,14 @@ cudaError_t rows_t(const paged::Args& a, const CUtensorMap& tk, const CUtensorMa
   const size_t sm = paged::RowsCfg<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(a.items, a.Hkv, a.S), 128 * MT + 32, sm, st>>>(tk, tv, a);
+  // kWhole: at most S pieces of cut items and one of every other, and none of fewer than min_split
+  // tiles of the longest possible stream
+  const long long items = (long long)a.items * a.Hkv, tiles = ceil_div64((long long)a.max_pages * a.page, paged::BNR);
+  long long pieces = a.B == 1 ? (items > a.S ? items : a.S) : items + a.S;
+  const long long most = items * (tiles / a.min_split > 1 ? tiles / a.min_split : 1);
+  pieces = pieces < most ? pieces : most;
+  const dim3 grid = KIND == paged::kWhole ? dim3((unsigned)pieces) : dim3(a.items, a.Hkv, a.S);
+  kern<<<grid, 128 * MT + 32, sm, st>>>(tk, tv, a);
   return cudaGetLastError();
 }
 template <typename T, int D>
@@ -489,8 +631,10 @@ cudaError_t rows_d(const paged::Args& a, const PagedPlan& pl, const CUtensorMap&
 
 template <typename T, int D>
 cudaError_t combine_t(const paged::Args& a, const PagedPlan& pl, cudaStream_t st) {
-  const dim3 grid(a.items, a.Hkv);
   const int rows = 16 * pl.mt;
+  // fewer than S items are cut (kWhole)
+  const long long items = (long long)a.items * a.Hkv;
+  const dim3 grid = pl.kind == paged::kUnits ? dim3(a.items, a.Hkv) : dim3((unsigned)(items < a.S ? items : a.S));
   if (pl.kind == paged::kUnits) return launch_early(paged::k_paged_combine<T, D, paged::kUnits>, grid, paged::kCombThreads, 0, st, a, rows);
   return launch_early(paged::k_paged_combine<T, D, paged::kWhole>, grid, paged::kCombThreads, 0, st, a, rows);
 }
@@ -498,7 +642,9 @@ cudaError_t combine_t(const paged::Args& a, const PagedPlan& pl, cudaStream_t st
 }  // namespace
 
 // Rows of an item: the unit's (or the longest sequence's) tokens times the heads that share a
-// key/value head.  Up to 32 go to the rows kernel, more to the 256-row tensor tiles.
+// key/value head.  Up to 32 go to the rows kernel, more to the 256-row tensor tiles: 32 rows of d 128
+// take 29 us against 39 us (2 x 8 heads of 8,192 keys), 69 against 71 us (8 x 8 heads) and 113
+// against 113 us (16 x 8 heads).
 PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int max_chunk, int q_block, bool sel) {
   PagedPlan p{};
   const long long G = Hq / Hkv;
@@ -525,13 +671,20 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int
   p.min_split = 4;
   p.S = 1;
   if (!p.rows) return p;
-  const long long most = ceil_div64(ceil_div64((long long)max_pages * page, kPagedRowsBN), p.min_split);
-  // Two CTAs per SM.  One sequence, or lists of equal length, fill one round of them: 256 lists of
-  // 64 pages of 64 keys take 126 us uncut and 145 us in four splits.  Sequences of unequal length
-  // take eight rounds, so that the last one is short: 48 sequences of 500 to 32,000 keys take
-  // 497 us, against 521 us with four rounds and 587 us uncut.
-  const long long want = B == 1 || sel ? 296 : 2368;
-  long long S = items * Hkv > 0 ? want / (items * Hkv) : 1;
+  const int once = p.mt == 1 ? 296 : 148;       // resident CTAs: two per SM, or one of 32 rows
+  if (!sel) {
+    // One round when the items alone do not fill the GPU, whatever their lengths (16 x 8 heads of
+    // 8,192 keys: 88 us, 91 us with two rounds, 97 us with four).  More items than that make a
+    // last round of uncut ones, which four rounds of pieces keep short (48 sequences of 500 to
+    // 32,000 keys: 494 us against 568 us; 64 equal ones of 8,192: 320 us against 304 us); of 32 rows
+    // two rounds do (32 x 8 heads of 1,024 keys: 45 us, 64 us with four).
+    p.S = items * Hkv < once ? once : (p.mt == 1 ? 4 : 2) * once;
+    return p;
+  }
+  // lists are equally long: one round of CTAs (256 lists of 64 pages of 64 keys take 126 us uncut
+  // and 145 us in four pieces)
+  const long long most = ceil_div64((long long)max_pages * page, kPagedRowsBN) / p.min_split;
+  long long S = items * Hkv > 0 ? once / (items * Hkv) : 1;
   S = S < most ? S : most;
   S = S < 64 ? S : 64;
   p.S = S < 1 ? 1 : (int)S;

@@ -138,12 +138,18 @@ def test_select_units(spr):
         spr.sparsepr_select_units(_cache(spr))
 
 
-def test_workspace_follows_the_splits(spr):
-    """One long sequence is split (partial results in the workspace), many sequences are not."""
-    one = _cache(spr, B=1, T=1, max_chunk=1, max_pages=1000, n_pages=1000)
-    many = _cache(spr, B=4096, T=4096, max_chunk=1, max_pages=1000, n_pages=100000)
-    assert spr.sparsepr_paged_workspace_bytes(one) > 1 * 8 * 64 * 4
-    assert spr.sparsepr_paged_workspace_bytes(many) == 256
+def test_workspace_holds_the_pieces(spr):
+    """Partial results of single tokens are a fixed number of pieces, not one per sequence; larger
+    chunks take the tile kernel's slots and plan, selections the scores of split lists."""
+    one = spr.sparsepr_paged_workspace_bytes(_cache(spr, B=1, T=1, max_chunk=1, max_pages=1000, n_pages=1000))
+    many = spr.sparsepr_paged_workspace_bytes(_cache(spr, B=4096, T=4096, max_chunk=1, max_pages=1000, n_pages=100000))
+    assert 256 < one < many <= 5 * one
+    chunk = _cache(spr, B=2, T=4000, max_chunk=2000, max_pages=1000, n_pages=2000)
+    assert spr.sparsepr_paged_workspace_bytes(chunk) > 2 * 148 * 256 * 64 * 4
+    plain = spr.sparsepr_paged_workspace_bytes(_cache(spr, B=1, T=1, max_chunk=1, max_pages=4000, n_pages=4000))
+    sel = spr.sparsepr_paged_workspace_bytes(_cache(spr, B=1, T=1, max_chunk=1, max_pages=4000, n_pages=4000, n_select=8,
+                                                    q_block=1))
+    assert sel >= plain + 2 * 4000 * 4
 
 
 def test_calls_refuse_before_cuda(spr):
