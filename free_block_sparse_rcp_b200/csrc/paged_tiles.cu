@@ -632,14 +632,10 @@ __global__ void __launch_bounds__(NTT, 1)
     float* mine = reinterpret_cast<float*>(smem + L::oEx) + (t * 2 + hv) * BM + r;
     const float* other = reinterpret_cast<const float*>(smem + L::oEx) + (t * 2 + (hv ^ 1)) * BM + r;
     const bool wide_rows = (((uintptr_t)a.O | (uintptr_t)(a.ost * 2) | (uintptr_t)(a.osh * 2)) & 31) == 0;
-    bool ok = true;
+    bool ok = true, out = false;      // out: left by a vote
     int tc = 0, use = 0;              // chunks and segments of this tile so far
     Seg g;
-    for (int i = 0;; ++i) {
-      // after a timeout the two warps of a row's threads may see different answers: they leave
-      // together, or one would wait at their barrier for ever
-      const bool got = ok && get_seg(i, g);
-      if (!bar_and(pair, 64, got)) break;
+    for (int i = 0; ok && get_seg(i, g); ++i) {
       const int ntile = g.nrows > BM ? 2 : 1;
       const bool in = row < g.nrows;
       const int nct = t < ntile ? (t == 0 ? g.nch0 : g.nch) : 0;
@@ -712,10 +708,11 @@ __global__ void __launch_bounds__(NTT, 1)
         named_sync(pair, 64);
       };
       for (int j = 0; j < nct; ++j) {
-        ok = waits(bars->s_full[t], (tc + j) & 1);
-        // both warps of the rows take the same way out
+        ok = ok && waits(bars->s_full[t], (tc + j) & 1);
+        // both warps of the rows take the same way out: after a timeout they may see different
+        // answers, and one that has left its loop votes against the other below
         if (!bar_and(pair, 64, ok)) {
-          ok = false;
+          out = true;
           break;
         }
         tc_fence_after();
@@ -753,13 +750,16 @@ __global__ void __launch_bounds__(NTT, 1)
         if (full) chunk(std::false_type{});
         else chunk(std::true_type{});
       }
-      if (ok && nct > 0) ok = waits(bars->o_done[t], use & 1);
-      tc_fence_after();
-      // the row's sum over both threads (the exchange slots are free: the last use was read before
-      // the chunk's barrier)
-      *mine = ok ? l : __int_as_float(0x7fffffff);
-      named_sync(pair, 64);
-      l = hv ? *other + *mine : *mine + *other;
+      if (out) break;
+      if (nct > 0) {
+        ok = ok && waits(bars->o_done[t], use & 1);
+        tc_fence_after();
+        // the row's sum over both threads (the exchange slots are free: their last use was read
+        // before the chunk's barrier)
+        *mine = ok ? l : __int_as_float(0x7fffffff);
+        named_sync(pair, 64);
+        l = hv ? *other + *mine : *mine + *other;
+      }
       const bool poison = g.bad != 0 || bad_page[i & 1] != 0 || !(l == l);
       const float inv = poison ? __int_as_float(0x7fffffff) : (l > 0.f ? 1.f / l : 0.f);
       const float z = poison ? __int_as_float(0x7fffffff)
@@ -817,11 +817,12 @@ __global__ void __launch_bounds__(NTT, 1)
         if (g.slot >= 0) a.part_lse[prow] = z;
         else if (a.lse) a.lse[qrow * a.Hq + qh] = z;
       }
-      named_sync(pair, 64);      // the sums have been exchanged before the next segment's maxima
+      if (nct > 0) named_sync(pair, 64);      // the sums have been read before the next segment's maxima
       tc += nct;
       use += nct > 0 ? 1 : 0;
       free_seg(i);
     }
+    if (!out) bar_and(pair, 64, false);
   }
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   tc_fence_before();
