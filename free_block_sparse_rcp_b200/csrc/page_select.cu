@@ -19,6 +19,9 @@
 // Work: the means are read once per unit (1 / page of the keys' bytes), 4 d operations per page;
 // the queries once.  One block per (unit, head), or several that share its pages when there are
 // few units; the selection then runs as a second kernel over the stored scores.
+// Measured: 32 units of 64 tokens x 8 heads over 1,024 pages (d 128) 25 us: finding
+// the unit 1.8, the mean query 5, the scores 11 (each unit reads its head's means: 64 MB from L2 at
+// 6 TB/s), the list 7.  Half the instructions per score took the same time.
 #include "paged.cuh"
 
 namespace spr {

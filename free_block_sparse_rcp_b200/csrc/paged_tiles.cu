@@ -25,6 +25,15 @@
 // in item order so that CTAs that run together share keys in L2, as long as the longest entry
 // allows it, and then a run of the chunks of the remaining entries, cut wherever the CTA's share
 // ends.  The pieces of a cut entry are joined by k_tiles_join.
+//
+// Bounds.  d = 128: a chunk of both tiles takes 1.65 us, and long calls run into the power limit besides:
+// 4,680 tokens x 40 heads over 32,760 keys take 2.65 ms, 1,130 TFLOP/s, the last 1,024-token frame of
+// 4 x 16 heads over 16,384 keys 545 us, 1,010 TFLOP/s (457 us in a single launch, before the clock
+// falls).  d = 64: half the products, as many exponentials: a chunk of both tiles takes 1.45 us, and
+// the unit that computes exponentials 1.18 us of it; six ragged chunks (87 GFLOP) take 173 us.
+// Measured without gain: keys in double-buffered halves (N = 64 products take as long as N = 128: 2.0
+// us per chunk), a quarter or half of the exponentials as polynomials in the FMA units, P handed
+// over warp by warp, pieces of two chunks.
 #include <cuda.h>
 
 #include <type_traits>
