@@ -145,6 +145,13 @@ __device__ __forceinline__ int item_count(int n, int G, int rows, int q_block, i
   return (int)(((long long)n + q_block - 1) / q_block) * ppu;
 }
 
+// Sums of counts that stop at 2^32 - 1: offsets out of order can promise more items than there are
+// rows, and a sum that wrapped would send a block to an item that its sequence does not have.
+__device__ __forceinline__ unsigned add_sat(unsigned a, unsigned b) {
+  const unsigned s = a + b;
+  return s < a ? 0xffffffffu : s;
+}
+
 // Sequence and rank of item `idx` (counted sequence by sequence), with the sequence's raw entries;
 // every thread of the block calls it, all get the result; b = -1 past the last item.  Each thread
 // takes a run of sequences, their counts are scanned, and the run that holds idx is walked by its
@@ -165,31 +172,34 @@ __device__ __forceinline__ Found find_item(const Args& a, int idx, int rows, int
     lo = min(max(lo, 0), a.T);
     return item_count<KIND>(max(0, min(hi, a.T) - lo), a.G, rows, a.q_block, ppu);
   };
-  int mine = 0, len0 = 0, lo0 = 0, hi0 = 0;
+  unsigned mine = 0;
+  int len0 = 0, lo0 = 0, hi0 = 0;
   for (int b = b0; b < b1; ++b) {
     lo0 = a.q_start[b];
     hi0 = a.q_start[b + 1];
     len0 = a.kv_len[b];
-    mine += items(lo0, hi0);
+    mine = add_sat(mine, (unsigned)items(lo0, hi0));
   }
-  int inc = mine;
+  mine = min(mine, 0x7fffffffu);
+  unsigned inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
+    const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc = add_sat(inc, v);
   }
-  if (lane == 31) sm[warp] = inc;
+  if (lane == 31) sm[warp] = (int)inc;
   if (tid == 0) sm[NT / 32] = -1;
   __syncthreads();
-  int at = inc - mine;
+  unsigned at = inc - mine;        // beyond every idx once the sum has stopped
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w)
-    if (w < warp) at += sm[w];
-  if (idx >= at && idx < at + mine) {
+    if (w < warp) at = add_sat(at, (unsigned)sm[w]);
+  const unsigned x = (unsigned)idx;
+  if (x >= at && x - at < mine) {
     int b = b0;
     for (; b + 1 < b1; ++b) {
-      const int c = items(a.q_start[b], a.q_start[b + 1]);
-      if (idx < at + c) break;
+      const unsigned c = (unsigned)items(a.q_start[b], a.q_start[b + 1]);
+      if (x - at < c) break;
       at += c;
     }
     if (b + 1 < b1) {
@@ -198,7 +208,7 @@ __device__ __forceinline__ Found find_item(const Args& a, int idx, int rows, int
       len0 = a.kv_len[b];
     }
     sm[NT / 32] = b;
-    sm[NT / 32 + 1] = idx - at;
+    sm[NT / 32 + 1] = (int)(x - at);
     sm[NT / 32 + 2] = lo0;
     sm[NT / 32 + 3] = hi0;
     sm[NT / 32 + 4] = len0;

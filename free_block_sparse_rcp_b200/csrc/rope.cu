@@ -444,28 +444,29 @@ __global__ void __launch_bounds__(kMeanThreads) k_page_means(AppendArgs a, int t
     const int lane = tid & 31, warp = tid >> 5;
     const int run = (a.B + kMeanThreads - 1) / kMeanThreads;
     const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
-    int mine = 0;
-    for (int i = b0; i < b1; ++i) mine += pages_of(i);
-    int inc = mine;
+    unsigned mine = 0;
+    for (int i = b0; i < b1; ++i) mine = paged::add_sat(mine, (unsigned)pages_of(i));
+    mine = min(mine, 0x7fffffffu);
+    unsigned inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc = paged::add_sat(inc, v);
     }
-    if (lane == 31) sm_find[warp] = inc;
+    if (lane == 31) sm_find[warp] = (int)inc;
     __syncthreads();
-    int at = inc - mine;
-    for (int w = 0; w < warp; ++w) at += sm_find[w];
+    unsigned at = inc - mine;      // beyond every index once the sum has stopped
+    for (int w = 0; w < warp; ++w) at = paged::add_sat(at, (unsigned)sm_find[w]);
     __syncthreads();
     if (tid == 0) sm_find[0] = -1;
     __syncthreads();
-    const int idx = blockIdx.x;
-    if (idx >= at && idx < at + mine) {
+    const unsigned x = blockIdx.x;
+    if (x >= at && x - at < mine) {
       for (int i = b0; i < b1; ++i) {
-        const int c = pages_of(i);
-        if (idx < at + c) {
+        const unsigned c = (unsigned)pages_of(i);
+        if (x - at < c) {
           sm_find[0] = i;
-          sm_find[1] = idx - at;
+          sm_find[1] = (int)(x - at);
           break;
         }
         at += c;

@@ -383,6 +383,28 @@ def test_q_start_out_of_order_is_an_error(spr, gpu):
     assert spr.sparsepr_paged_error(s.ws) == 1
 
 
+def test_q_start_that_promises_more_than_there_is(spr, gpu):
+    """Offsets that go back to 0 again and again count 2^32 units: an error, and every list that is
+    written is one of the cache's."""
+    B, T = 65536, 131072
+    s = Scene(spr, gpu, [1], [64], Hq=1, Hkv=1, d=64, page=16, dt=BF, seed=16)
+    p = spr.CacheParams.make(B, 1, 1, 64, page=16, n_pages=s.n_pages, max_pages=4, T=T, max_chunk=1, q_block=1, n_select=2)
+    q_start = torch.tensor([0, T], dtype=torch.int32).repeat(B // 2 + 1)[:B + 1].to(gpu)
+    kv_len = torch.full((B,), 64, dtype=torch.int32, device=gpu)
+    table = s.dev["table"].expand(B, 4).contiguous()
+    Q = s.dev["Q"].expand(T, 1, 64).contiguous()
+    ws = spr.paged_workspace(p, gpu)
+    sel, cnt = spr.alloc_selection(p, gpu)
+    sel.fill_(-9)
+    cnt.fill_(-9)
+    spr.sparsepr_page_select(p, Q, q_start, kv_len, table, s.dev["km"], sel, cnt, ws)
+    assert int(cnt.max()) <= 2 and int(sel.max()) <= 3
+    spr.sparsepr_paged_clear_error(ws)
+    O = torch.zeros_like(Q)
+    spr.sparsepr_paged_attention(p, Q, q_start, kv_len, table, s.dev["kp"], s.dev["vp"], O, None, ws, sel=sel, sel_count=cnt)
+    assert spr.sparsepr_paged_error(ws) == 1
+
+
 def test_far_offsets(spr, gpu):
     """Pages past 2^31 elements of the pool, and queries past 2^31 elements of a strided buffer."""
     d, page, Hkv = 128, 128, 8
