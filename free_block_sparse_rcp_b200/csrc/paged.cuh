@@ -105,7 +105,7 @@ struct Args {
   int* err;
   int B, Hq, Hkv, G, page, n_pages, max_pages, T, max_chunk, frame;
   int q_block, n_select;
-  int ppu;               // row parts per unit (selection, tensor-tile kernel), else 1
+  int ppu;               // row parts per unit (rows kernel, whole sequences: at most, per sequence)
   int items;             // upper bound of the (sequence, unit, part) items of a head
   int S, min_split;      // rows kernel: pieces to aim for (whole sequences) or pieces of a list at most;
                          // fewest tiles of a piece
@@ -331,7 +331,8 @@ struct PagedPlan {
   int kind;         // paged::ItemKind
   int ppu, items, S, min_split;
 };
-PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int max_chunk, int q_block, bool sel);
+PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int max_chunk, int q_block, int n_select,
+                     bool sel);
 cudaError_t launch_paged_rows(const paged::Args& a, const PagedPlan& pl, int d, int dtype, const void* kp,
                               const void* vp, cudaStream_t st);
 cudaError_t launch_paged_tiles(const paged::Args& a, const PagedPlan& pl, int d, int dtype, const void* kp,

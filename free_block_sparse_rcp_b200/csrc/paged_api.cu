@@ -199,7 +199,7 @@ void strides2(const long long* s, int heads, int d, long long& t, long long& h) 
 }
 
 PagedPlan plan_of(const sparsepr_cache_params& p, bool sel) {
-  return paged_plan(p.B, p.Hq, p.Hkv, p.page, p.max_pages, p.T, p.max_chunk, p.q_block, sel);
+  return paged_plan(p.B, p.Hq, p.Hkv, p.page, p.max_pages, p.T, p.max_chunk, p.q_block, p.n_select, sel);
 }
 
 int select_units(const sparsepr_cache_params& p) {

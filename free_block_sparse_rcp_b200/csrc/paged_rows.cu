@@ -72,49 +72,54 @@ __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
 struct Item {
   Seq s;
   int h;                   // key/value head
-  int tok0, ntok;          // tokens of the sequence in this item
+  int tok0;                // first token of the sequence (or of its unit)
+  int row0, nrows;         // this item's rows among those of the sequence (unit)
   const int* list;         // page list (NULL: the whole cache)
   int cnt, total;          // list entries; keys of the stream
   int ns, part, slot;      // pieces of the item, this piece, first piece's slot of partial results
   bool bad;
 };
 
-// Pieces of whole sequences.  Of `target` pieces, sequence b with t_b tiles of keys per head gets
-// floor(target t_b / sum t Hkv) per head, at least one and none of fewer than min_split tiles: no
-// more than target pieces are of cut items, which is what the partial results have slots for, and
-// pieces are about equally long however unequal the sequences are.  Every block computes this from
+// Pieces of whole sequences.  Sequence b has parts_b items of R rows per head, each of t_b tiles of
+// keys (at most).  Of `target` pieces each gets floor(target t_b / sum t parts Hkv), at least one and
+// none of fewer than min_split of t_b's tiles: no more than target pieces are of cut items, which is
+// what the partial results have slots for, and pieces are about equally long however unequal the
+// sequences are.  Every block computes this from
 // q_start and kv_len.  By piece (JOIN false): the idx-th piece; by item (JOIN true): the idx-th cut
 // item.  ns = 0: there is none.
 struct Piece {
-  int b, h, part, ns, slot, lo, hi, len;
+  int b, h, rows, part, ns, slot, lo, hi, len;     // rows: which of the sequence's items
 };
 template <int NT, bool JOIN>
-__device__ __forceinline__ Piece find_piece(const Args& a, int idx, int* sm /* [3 NT / 32 + 8] */) {
+__device__ __forceinline__ Piece find_piece(const Args& a, int idx, int R, int* sm /* [3 NT / 32 + 8] */) {
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (a.B + NT - 1) / NT;
   const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+  int parts = 1;
   auto tiles_of = [&](int b, int& lo, int& hi, int& len) -> int {    // -1: no new tokens
     lo = a.q_start[b];
     hi = a.q_start[b + 1];
     len = a.kv_len[b];
     const Seq s = make_seq(a, b, lo, hi, len);
     if (s.n <= 0) return -1;
+    // (more tokens than max_chunk: an error, and not more items than were counted on)
+    if (a.ppu > 1) parts = (int)min((long long)a.ppu, ((long long)s.n * a.G + R - 1) / R);
     return (visible_end(s.len - 1, a.frame, s.len) + BNR - 1) / BNR;
   };
   int lo = 0, hi = 0, len = 0, t = -1;
   if (a.B == 1) {        // nothing to count
     t = tiles_of(0, lo, hi, len);
-    int ns = t < 0 ? 0 : max(1, min(t / a.min_split, a.S / a.Hkv));
+    int ns = t < 0 ? 0 : max(1, min(t / a.min_split, a.S / a.Hkv / parts));
     if (JOIN && ns <= 1) ns = 0;
-    if (idx >= a.Hkv * (JOIN ? 1 : ns)) ns = 0;
-    const int h = ns == 0 ? 0 : (JOIN ? idx : idx / ns);
-    return Piece{0, h, ns == 0 || JOIN ? 0 : idx - h * ns, ns, h * ns, lo, hi, len};
+    if (idx >= (long long)a.Hkv * parts * (JOIN ? 1 : ns)) ns = 0;
+    const int item = ns == 0 ? 0 : (JOIN ? idx : idx / ns), h = parts == 1 ? item : item / parts;
+    return Piece{0, h, item - h * parts, ns == 0 || JOIN ? 0 : idx - item * ns, ns, item * ns, lo, hi, len};
   }
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     t = tiles_of(b, lo, hi, len);
-    mine += max(t, 0);
+    mine += (long long)max(t, 0) * parts;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -136,8 +141,8 @@ __device__ __forceinline__ Piece find_piece(const Args& a, int idx, int* sm /* [
   for (int b = b0; b < b1; ++b) {
     if (run > 1) t = tiles_of(b, lo, hi, len);
     const int ns = pieces_of(t);
-    np += JOIN ? (ns > 1) : ns;
-    nc += ns > 1 ? ns : 0;
+    np += parts * (JOIN ? (ns > 1) : ns);
+    nc += ns > 1 ? parts * ns : 0;
   }
   int ip = np, ic = nc;
 #pragma unroll
@@ -169,7 +174,7 @@ __device__ __forceinline__ Piece find_piece(const Args& a, int idx, int* sm /* [
     for (int b = b0; b < b1; ++b) {
       if (run > 1) t = tiles_of(b, lo, hi, len);
       const int ns = pieces_of(t);
-      const int c = JOIN ? (ns > 1) : ns;
+      const int c = parts * (JOIN ? (ns > 1) : ns);
       if (at < (long long)(ap + c) * a.Hkv) {
         f[0] = b;
         f[1] = ns;
@@ -178,10 +183,11 @@ __device__ __forceinline__ Piece find_piece(const Args& a, int idx, int* sm /* [
         f[4] = lo;
         f[5] = hi;
         f[6] = len;
+        f[7] = parts;
         break;
       }
       ap += c;
-      ac += ns > 1 ? ns : 0;
+      ac += ns > 1 ? parts * ns : 0;
     }
   }
   __syncthreads();
@@ -189,57 +195,66 @@ __device__ __forceinline__ Piece find_piece(const Args& a, int idx, int* sm /* [
   p.b = f[0];
   p.ns = f[1];
   if (p.ns == 0) return p;
-  const int local = f[2];
-  p.h = JOIN ? local : local / p.ns;
-  p.part = JOIN ? 0 : local - p.h * p.ns;
-  p.slot = f[3] + p.h * p.ns;
+  const int item = JOIN ? f[2] : f[2] / p.ns;
+  parts = f[7];
+  p.h = parts == 1 ? item : item / parts;
+  p.rows = item - p.h * parts;
+  p.part = JOIN ? 0 : f[2] - item * p.ns;
+  p.slot = f[3] + item * p.ns;
   p.lo = f[4];
   p.hi = f[5];
   p.len = f[6];
   return p;
 }
 
-// kWhole: block x is a piece (or, JOIN, a cut item); kUnits: block (x, y, z) is piece z of the list
-// of unit x and head y.  False: nothing to do.
+// kWhole: block x is a piece (or, JOIN, a cut item); kUnits: block (x, y, z) is piece z of item x (a
+// unit, or R of its rows) and head y.  False: nothing to do.
 template <int KIND, int NT, bool JOIN>
-__device__ __forceinline__ bool load_item(const Args& a, int* sm /* [3 NT / 32 + 8] */, Item& it) {
+__device__ __forceinline__ bool load_item(const Args& a, int R, int* sm /* [3 NT / 32 + 8] */, Item& it) {
   it.list = nullptr;
   it.cnt = 0;
   if (KIND == kWhole) {
-    const Piece p = find_piece<NT, JOIN>(a, blockIdx.x, sm);
+    const Piece p = find_piece<NT, JOIN>(a, blockIdx.x, R, sm);
     if (p.ns == 0) return false;
     it.s = make_seq(a, p.b, p.lo, p.hi, p.len);
     it.bad = it.s.bad;
     it.h = p.h;
     it.tok0 = 0;
-    it.ntok = it.s.n;
+    it.row0 = p.rows * R;
+    it.nrows = (int)min((long long)R, (long long)it.s.n * a.G - it.row0);
     it.ns = p.ns;
     it.part = p.part;
     it.slot = p.slot;
-    it.total = visible_end(it.s.len - 1, a.frame, it.s.len);
+    it.total = visible_end(it.s.len - it.s.n + (it.row0 + it.nrows - 1) / a.G, a.frame, it.s.len);
     return true;
   }
-  const Found f = find_item<KIND, NT>(a, blockIdx.x, 0, 1, sm);
+  const Found f = find_item<KIND, NT>(a, blockIdx.x, 0, a.ppu, sm);
   if (f.b < 0) return false;
   it.s = make_seq(a, f.b, f.lo, f.hi, f.len);
   it.bad = it.s.bad;
   it.h = blockIdx.y;
-  it.tok0 = f.rank * a.q_block;
-  it.ntok = min(a.q_block, it.s.n - it.tok0);
-  const size_t at = (size_t)blockIdx.x * a.Hkv + it.h;
+  const int unit = a.ppu == 1 ? f.rank : f.rank / a.ppu;
+  it.tok0 = unit * a.q_block;
+  it.row0 = (f.rank - unit * a.ppu) * R;
+  const int ntok = min(a.q_block, it.s.n - it.tok0);
+  it.nrows = (int)min((long long)R, (long long)ntok * a.G - it.row0);
+  const size_t at = (size_t)(a.ppu == 1 ? blockIdx.x : blockIdx.x / a.ppu) * a.Hkv + it.h;
   it.list = a.sel + at * a.n_select;
   const int c = a.sel_cnt[at];
   it.cnt = min(max(c, 0), a.n_select);
   it.bad |= c != it.cnt;
-  if (it.ntok <= 0) return false;
-  const int end = visible_end(it.s.len - it.s.n + it.tok0 + it.ntok - 1, a.frame, it.s.len);
+  if (it.nrows <= 0) return false;
+  const int end = visible_end(it.s.len - it.s.n + it.tok0 + ntok - 1, a.frame, it.s.len);
   int seen = it.cnt;
   it.total = stream_limit(end, it.list, it.cnt, a.page, &seen);
   // the unit's last token sees every page of its list, and no page is there twice
   it.bad |= seen != it.cnt || it.total > end;
+  const int last = it.tok0 + (it.row0 + it.nrows - 1) / a.G;       // of these rows
+  if (a.ppu > 1 && a.frame != 0)
+    it.total = min(it.total, stream_limit(visible_end(it.s.len - it.s.n + last, a.frame, it.s.len), it.list, it.cnt, a.page));
   it.ns = split_count((it.total + BNR - 1) / BNR, a.S, a.min_split);
   it.part = JOIN ? 0 : blockIdx.z;
-  it.slot = (int)(at * a.S);
+  it.slot = (int)(((size_t)blockIdx.x * a.Hkv + it.h) * a.S);
   return JOIN ? it.ns > 1 : it.part < it.ns;
 }
 
@@ -276,7 +291,7 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
     return;
   }
   Item it;
-  if (!load_item<KIND, NT, false>(a, s_find, it)) return;
+  if (!load_item<KIND, NT, false>(a, 16 * MT, s_find, it)) return;
   const int tiles = (it.total + BNR - 1) / BNR, ns = it.ns, h = it.h;
   const int t0 = split_at(tiles, it.part, ns), t1 = split_at(tiles, it.part + 1, ns);
   if (tid == 0) {
@@ -290,7 +305,7 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
     fence_barrier_init();
   }
   __syncthreads();
-  const int nrows = min(it.ntok * a.G, 16 * MT);
+  const int nrows = it.nrows;
 
   if (warp == NW) {
     // ---------------- producer ----------------
@@ -333,6 +348,14 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
     __syncwarp();
   } else {
     // ---------------- 16 rows x 16-key slices ----------------
+    if (KIND == kUnits && a.ppu > 1)
+      // these rows may end before a wrong entry, which is read as it comes otherwise: the list is
+      // the unit's, and so is its error
+      for (int k = tid; k < it.cnt; k += 128 * MT)
+        if (it.list[k] <= (k > 0 ? it.list[k - 1] : -1)) {
+          s_bad = 1;
+          set_error(a.err, DERR_INDEX);
+        }
     const int mt = warp >> 2, sl = warp & 3;
     const int g = lane >> 2, q2 = (lane & 3) * 2;
     uint32_t qf[D / 16][4];
@@ -341,7 +364,7 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
     for (int r = 0; r < 2; ++r) {
       const int row = mt * 16 + g + 8 * r;
       const bool in = row < nrows;
-      const int tok = in ? row / a.G : 0, gh = in ? row - tok * a.G : 0;
+      const int tok = in ? (it.row0 + row) / a.G : 0, gh = in ? it.row0 + row - tok * a.G : 0;
       const T* qp = (const T*)a.Q + (long long)(it.s.q0 + it.tok0 + tok) * a.qst + (long long)(h * a.G + gh) * a.qsh;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -508,7 +531,7 @@ __global__ void __launch_bounds__(128 * MT + 32) k_paged_rows(const __grid_const
       float inv = ls[r] > 0.f ? 1.f / ls[r] : 0.f;
       float z = ls[r] > 0.f ? (ms[r] - SHIFT + log2f(ls[r])) * 0.69314718055994531f : -INFINITY;
       if (!(ls[r] == ls[r]) || poison) inv = z = __int_as_float(0x7fffffff);
-      const int tok = row / a.G, gh = row - tok * a.G;
+      const int tok = (it.row0 + row) / a.G, gh = it.row0 + row - tok * a.G;
       const long long qrow = it.s.q0 + it.tok0 + tok;
       const int qh = h * a.G + gh;
       const size_t prow = (size_t)(it.slot + it.part) * (16 * MT) + row;      // [slot][16 MT rows]
@@ -540,12 +563,12 @@ __global__ void __launch_bounds__(kCombThreads) k_paged_combine(Args a, int max_
   __shared__ __align__(8) int s_find[3 * kCombThreads / 32 + 8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Item it;
-  const bool any = load_item<KIND, kCombThreads, true>(a, s_find, it);
+  const bool any = load_item<KIND, kCombThreads, true>(a, max_rows, s_find, it);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the parts are complete
   if (!any) return;
-  const int nrows = min(it.ntok * a.G, max_rows), ns = it.ns, h = it.h;
+  const int nrows = it.nrows, ns = it.ns, h = it.h;
   for (int r = warp; r < nrows; r += kCombThreads / 32) {
-    const int tok = r / a.G, qh = h * a.G + (r - tok * a.G);
+    const int tok = (it.row0 + r) / a.G, qh = h * a.G + (it.row0 + r - tok * a.G);
     const size_t qrow = (size_t)it.s.q0 + it.tok0 + tok, prow = (size_t)it.slot * max_rows + r, step = max_rows;
     const float* po = a.part_o + prow * D + lane * (D / 32);
     constexpr int UN = 16;              // parts in flight; the first ones beside their lse
@@ -646,22 +669,37 @@ cudaError_t combine_t(const paged::Args& a, const PagedPlan& pl, cudaStream_t st
 
 }  // namespace
 
-// Rows of an item: the unit's (or the longest sequence's) tokens times the heads that share a
-// key/value head.  Up to 32 go to the rows kernel, more to the 256-row tensor tiles: 32 rows of d 128
-// take 29 us against 39 us (2 x 8 heads of 8,192 keys), 69 against 71 us (8 x 8 heads) and 113
-// against 113 us (16 x 8 heads).
-PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int max_chunk, int q_block, bool sel) {
+// Rows: the unit's (or the longest sequence's) tokens times the heads that share a key/value head.  Up
+// to 32 are one item of the rows kernel, whatever the work: 32 rows of d 128 take 29 us there against
+// 39 us in the 256-row tensor tiles (2 x 8 heads of 8,192 keys), 69 against 71 us (8 x 8 heads) and
+// 113 against 113 us (16 x 8 heads).  More rows are cut into items of 32 as long as the call is small:
+// the tiles' plan, their first chunks and their join take 20 us of latency, which the rows kernel
+// does not have, and their rate counts beyond that.  By pairs of query row and key (as many as the
+// pages and lists could hold), rows against tiles: 49 tokens x 2 heads, 383 keys (4 10^4) 10.8
+// against 20.1 us; 70 x 8, 2,112 keys (10^6) 17.6 against 32.0; 978 x 8, 848 keys (7 10^6) 32.6
+// against 33.4; 889 x 4, 6,904 keys (2 10^7) 88 against 39.  Lists, with their selection: 35 x 32, 5
+// pages of 128 (7 10^5) 28 against 38 us; 577 x 2, 64 of 32 (2 10^6) 42 against 43; 180 x 32, 33 of 16
+// (3 10^6) 63 against 57.
+PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int max_chunk, int q_block, int n_select,
+                     bool sel) {
   PagedPlan p{};
   const long long G = Hq / Hkv;
   const long long tok = sel && q_block < max_chunk ? q_block : max_chunk;
   const long long rows = tok * G;
-  p.rows = rows <= 32;
+  const long long pairs = (long long)T * Hq * ((sel ? n_select : max_pages) * (long long)page);
+  p.rows = rows <= 32 || pairs <= (sel ? 2000000 : 5000000);
   p.mt = rows <= 16 ? 1 : 2;
   p.ppu = 1;
   const long long units = sel ? ((long long)T + (q_block - 1ll) * B) / q_block : B;   // sum of ceil(n / q_block)
   long long items = units < T || !sel ? units : T;
   if (p.rows) {
     p.kind = sel ? paged::kUnits : paged::kWhole;
+    if (rows > 32) {
+      p.ppu = (int)ceil_div64(rows, 32);
+      // kWhole: sum of ceil(n G / 32), at most ppu each
+      const long long all = sel ? items * p.ppu : ((long long)T * G + 31ll * B) / 32, most = items * p.ppu;
+      items = all < most ? all : most;
+    }
   } else if (sel) {
     p.kind = paged::kUnits;
     p.ppu = (int)ceil_div64(rows, kPagedTileRows);

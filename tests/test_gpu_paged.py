@@ -170,17 +170,20 @@ def test_rope_gradient(spr, gpu):
 # ---------------------------------------------------------------------------
 class Scene:
     """A cache of sequences of kv rows, of which new are new; pages in random order.  Slots past
-    the rows in use hold NaN."""
+    the rows in use hold NaN.  tiles: so many packed rows behind the last sequence that the call
+    counts as a large one, whose chunks go to the tensor tiles."""
 
     def __init__(self, spr, gpu, new, kv, *, Hq, Hkv, d, page, dt, frame=1, q_block=0, n_select=0, n_sink=0, n_recent=0,
-                 seed=0, tail_rows=0, max_pages=None, max_chunk=None, spare=2, bump=0.0):
+                 seed=0, tail_rows=0, max_pages=None, max_chunk=None, spare=2, bump=0.0, tiles=False):
         g = gen(seed)
         self.new, self.kv, self.gpu, self.spr = new, kv, gpu, spr
         B = len(new)
-        self.T = sum(new) + tail_rows
         pages = [-(-k // page) for k in kv]
         self.n_pages = sum(pages) + spare
         mp = max(max(pages), 1) if max_pages is None else max_pages
+        self.T = sum(new) + tail_rows
+        if tiles:
+            self.T = max(self.T, 5_000_000 // (Hq * page * (min(mp, n_select) if n_select else mp)) + 1)
         order = torch.randperm(self.n_pages, generator=g).to(torch.int32)
         self.table = torch.full((B, mp), 2 ** 31 - 1, dtype=torch.int32)
         at = 0
@@ -260,6 +263,8 @@ ROWS = [   # new, kv, Hq, Hkv, d, page, dtype, frame
     ([5, 5], [77, 1000], 3, 1, 64, 64, BF, 0),                    # group of 3, no mask
     ([16, 9], [100, 40], 2, 2, 128, 32, BF, 1),
     ([1] * 40, [17 * i % 900 for i in range(40)], 2, 1, 64, 16, BF, 1),
+    ([1, 2], [700, 90], 40, 1, 128, 16, BF, 1),                   # a token's heads in two items
+    ([19, 0, 3] * 120, [20 + 7 * i % 150 for i in range(360)], 2, 1, 64, 16, FP, 1),   # many sequences, some of two items
 ]
 TILES = [
     ([40], [40], 1, 1, 64, 16, BF, 1),
@@ -274,20 +279,23 @@ TILES = [
 ]
 
 
-@pytest.mark.parametrize("case", ROWS + TILES, ids=lambda c: "-".join(str(x) for x in c))
-def test_attention(spr, gpu, case):
+@pytest.mark.parametrize("case,tiles", [(c, False) for c in ROWS + TILES] + [(c, True) for c in TILES],
+                         ids=lambda c: "-".join(str(x) for x in c) if isinstance(c, tuple) else ("tiles" if c else "rows"))
+def test_attention(spr, gpu, case, tiles):
     new, kv, Hq, Hkv, d, page, dt, frame = case
-    s = Scene(spr, gpu, new, kv, Hq=Hq, Hkv=Hkv, d=d, page=page, dt=dt, frame=frame, tail_rows=3, seed=len(kv) + d)
+    s = Scene(spr, gpu, new, kv, Hq=Hq, Hkv=Hkv, d=d, page=page, dt=dt, frame=frame, tail_rows=3, seed=len(kv) + d,
+              tiles=tiles)
     O, z = s.attend()
     s.check(O, z)
     O2, _ = s.attend(lse=False)
     assert torch.equal(O, O2)
 
 
-@pytest.mark.parametrize("new,kv,Hq,Hkv", [([1], [3000], 4, 1), ([70], [2500], 2, 2), ([1, 2], [1900, 10], 8, 4)])
-def test_attention_logits_that_move(spr, gpu, new, kv, Hq, Hkv):
+@pytest.mark.parametrize("new,kv,Hq,Hkv,tiles", [([1], [3000], 4, 1, False), ([70], [2500], 2, 2, False),
+                                                 ([70], [2500], 2, 2, True), ([1, 2], [1900, 10], 8, 4, False)])
+def test_attention_logits_that_move(spr, gpu, new, kv, Hq, Hkv, tiles):
     """Large logits, growing along the keys: the running maximum moves and early chunks vanish."""
-    s = Scene(spr, gpu, new, kv, Hq=Hq, Hkv=Hkv, d=64, page=32, dt=FP, frame=1, seed=9)
+    s = Scene(spr, gpu, new, kv, Hq=Hq, Hkv=Hkv, d=64, page=32, dt=FP, frame=1, seed=9, tiles=tiles)
     for b, n in enumerate(kv):
         for j in range(-(-n // 32)):
             s.kp[int(s.table[b, j])] *= 0.2 + 4.0 * j * 32 / n
@@ -296,10 +304,10 @@ def test_attention_logits_that_move(spr, gpu, new, kv, Hq, Hkv):
     s.check(*s.attend())
 
 
-@pytest.mark.parametrize("new,kv", [([1], [20000]), ([40], [9000])])
-def test_attention_many_small_weights_fp16(spr, gpu, new, kv):
+@pytest.mark.parametrize("new,kv,tiles", [([1], [20000], False), ([40], [9000], False), ([40], [9000], True)])
+def test_attention_many_small_weights_fp16(spr, gpu, new, kv, tiles):
     """One key far above thousands of equal others: their probabilities of 2^-18 still count."""
-    s = Scene(spr, gpu, new, kv, Hq=1, Hkv=1, d=64, page=64, dt=FP, frame=0, seed=3)
+    s = Scene(spr, gpu, new, kv, Hq=1, Hkv=1, d=64, page=64, dt=FP, frame=0, seed=3, tiles=tiles)
     s.kp.zero_()
     s.Q.zero_()
     s.Q[:, :, 0] = 10.0
@@ -310,18 +318,23 @@ def test_attention_many_small_weights_fp16(spr, gpu, new, kv):
     s.check(*s.attend())
 
 
-def test_a_list_longer_than_the_cache_is_an_error(spr, gpu):
+@pytest.mark.parametrize("tiles", [False, True])
+def test_a_list_longer_than_the_cache_is_an_error(spr, gpu, tiles):
     """Every page once and the last one again, behind the chunks that the visible keys need."""
-    s = Scene(spr, gpu, [40], [1280], Hq=2, Hkv=1, d=64, page=128, dt=BF, frame=0, q_block=40, n_select=12, seed=25)
-    sel = torch.tensor([[list(range(10)) + [9, 9]]], dtype=torch.int32, device=gpu)
-    O, _ = s.attend(sel, torch.full((1, 1), 12, dtype=torch.int32, device=gpu))
-    assert spr.sparsepr_paged_error(s.ws) == 1 and torch.isnan(O).all()
+    s = Scene(spr, gpu, [40], [1280], Hq=2, Hkv=1, d=64, page=128, dt=BF, frame=0, q_block=40, n_select=12, seed=25,
+              tiles=tiles)
+    sel, cnt = spr.alloc_selection(s.p, gpu)
+    sel[0, 0] = torch.tensor(list(range(10)) + [9, 9], dtype=torch.int32, device=gpu)
+    cnt[0, 0] = 12
+    O, _ = s.attend(sel, cnt)
+    assert spr.sparsepr_paged_error(s.ws) == 1 and torch.isnan(O[:40]).all()
 
 
+@pytest.mark.parametrize("tiles", [False, True])
 @pytest.mark.parametrize("new,kv,d", [([2], [700], 64), ([50], [700], 64), ([50], [700], 128)])
-def test_attention_large_values(spr, gpu, new, kv, d):
+def test_attention_large_values(spr, gpu, new, kv, d, tiles):
     """Values of 10^30 with a maximum that grows by thirty powers of two along the keys."""
-    s = Scene(spr, gpu, new, kv, Hq=2, Hkv=1, d=d, page=32, dt=BF, frame=0, seed=35)
+    s = Scene(spr, gpu, new, kv, Hq=2, Hkv=1, d=d, page=32, dt=BF, frame=0, seed=35, tiles=tiles)
     s.Q.fill_(0)
     s.Q[:, :, 0] = 8.0
     for j in range(22):
@@ -331,25 +344,26 @@ def test_attention_large_values(spr, gpu, new, kv, d):
     s.check(*s.attend())
 
 
-@pytest.mark.parametrize("new,kv", [([1, 1], [300, 70]), ([90], [400])])
-def test_attention_strided(spr, gpu, new, kv):
+@pytest.mark.parametrize("new,kv,tiles", [([1, 1], [300, 70], False), ([90], [400], False), ([90], [400], True)])
+def test_attention_strided(spr, gpu, new, kv, tiles):
     """Q and O as views of head-major and fused tensors."""
-    s = Scene(spr, gpu, new, kv, Hq=4, Hkv=2, d=64, page=32, dt=BF, seed=4)
+    s = Scene(spr, gpu, new, kv, Hq=4, Hkv=2, d=64, page=32, dt=BF, seed=4, tiles=tiles)
     O, z = s.attend()
     s.check(O, z)
     qh = s.dev["Q"].transpose(0, 1).contiguous().transpose(0, 1)
     fused = torch.zeros(s.T, 3, 4, 64, dtype=BF, device=gpu)
     O2, z2 = s.attend(O=fused[:, 1], Q=qh)
-    assert torch.equal(O2, O) and torch.equal(z2, z)
+    n = sum(new)
+    assert torch.equal(O2[:n], O[:n]) and torch.equal(z2, z) and torch.all(O2[n:] == 0)
     assert torch.all(fused[:, 0] == 0) and torch.all(fused[:, 2] == 0)
 
 
-@pytest.mark.parametrize("new", [[1, 1, 1], [40, 50, 45]])
-def test_attention_bad_inputs_are_errors(spr, gpu, new):
+@pytest.mark.parametrize("new,tiles", [([1, 1, 1], False), ([40, 50, 45], False), ([40, 50, 45], True)])
+def test_attention_bad_inputs_are_errors(spr, gpu, new, tiles):
     """Bad page ids and lengths: error 1, NaN in the rows that depend on them, the others right."""
     kv = [200, 150, 90]
     for what in ("page", "negative", "len", "chunk"):
-        s = Scene(spr, gpu, new, kv, Hq=2, Hkv=1, d=64, page=32, dt=BF, seed=5)
+        s = Scene(spr, gpu, new, kv, Hq=2, Hkv=1, d=64, page=32, dt=BF, seed=5, tiles=tiles)
         t, ln = s.table.clone(), s.kv_len.clone()
         if what == "page":
             t[1, 2] = s.n_pages
@@ -417,13 +431,14 @@ def test_far_offsets(spr, gpu):
     kp[shift:], vp[shift:], km[shift:] = s.dev["kp"], s.dev["vp"], s.dev["km"]
     table = s.table.clone()
     table[table < s.n_pages] += shift
-    for chunk, q_rows in ((40, slice(0, 41)), (1, slice(0, 1))):
+    for mp in (table.shape[1], 150):       # 150: a large call, to the tensor tiles
         p = spr.CacheParams.from_buffer_copy(s.p)
-        p.n_pages, p.max_chunk = n_pages, 40
+        p.n_pages, p.max_pages = n_pages, mp
         O, z = torch.empty_like(s.dev["Q"]), torch.empty(41, 8, device=gpu)
         ws = spr.paged_workspace(p, gpu)
-        spr.sparsepr_paged_attention(p, s.dev["Q"], s.dev["q_start"], s.dev["kv_len"], table.to(gpu), kp, vp, O, z, ws)
-    s.check(O, z)
+        t = torch.cat([table, table[:, :1].expand(2, mp - table.shape[1])], 1).to(gpu).contiguous()
+        spr.sparsepr_paged_attention(p, s.dev["Q"], s.dev["q_start"], s.dev["kv_len"], t, kp, vp, O, z, ws)
+        s.check(O, z)
     # append there too
     p = spr.CacheParams.from_buffer_copy(s.p)
     p.n_pages = n_pages
@@ -568,14 +583,16 @@ SELECT = [  # new, kv, Hq, Hkv, d, page, dtype, frame, q_block, n_select, n_sink
     ([20], [8], 1, 1, 64, 16, BF, 1, 4, 3, 1, 1),                 # units that see no page
     ([300], [600], 4, 1, 64, 32, BF, 1, 100, 9, 1, 2),            # units of several row parts
     ([3, 3], [90, 200], 16, 1, 64, 16, BF, 1, 2, 4, 1, 1),        # 32 rows per unit
+    ([1, 3], [900, 64], 48, 1, 128, 16, FP, 1, 1, 6, 0, 1),       # a token's heads in two items
 ]
 
 
-@pytest.mark.parametrize("case", SELECT, ids=lambda c: "-".join(str(x) for x in c))
-def test_select_and_attend(spr, gpu, case):
+@pytest.mark.parametrize("case,tiles", [(c, False) for c in SELECT] + [(c, True) for c in SELECT if min(c[8], max(c[0])) * c[2] > 32 * c[3]],
+                         ids=lambda c: "-".join(str(x) for x in c) if isinstance(c, tuple) else ("tiles" if c else "rows"))
+def test_select_and_attend(spr, gpu, case, tiles):
     new, kv, Hq, Hkv, d, page, dt, frame, qb, ns, sink, recent = case
     s = Scene(spr, gpu, new, kv, Hq=Hq, Hkv=Hkv, d=d, page=page, dt=dt, frame=frame, q_block=qb, n_select=ns, n_sink=sink,
-              n_recent=recent, seed=21, bump=0.7, tail_rows=2)
+              n_recent=recent, seed=21, bump=0.7, tail_rows=2, tiles=tiles)
     sel, cnt = s.select()
     want, wc = R.select(s.Q, new, kv, s.table, s.km, page, frame, qb, ns, sink, recent)
     n = want.shape[0]
@@ -669,9 +686,10 @@ def test_select_many_pages(spr, gpu, Hkv):
 
 
 def test_bad_lists_are_errors(spr, gpu):
-    for new in ([1, 1], [40, 40]):
+    for new, tiles in (([1, 1], False), ([40, 40], False), ([40, 40], True)):
         for what in ("order", "range", "count", "negative", "twice"):
-            s = Scene(spr, gpu, new, [300, 300], Hq=2, Hkv=1, d=64, page=16, dt=BF, q_block=40, n_select=6, n_recent=1, seed=25)
+            s = Scene(spr, gpu, new, [300, 300], Hq=2, Hkv=1, d=64, page=16, dt=BF, q_block=40, n_select=6, n_recent=1, seed=25,
+                      tiles=tiles)
             sel, cnt = s.select()
             good, _ = s.attend(sel, cnt)
             if what == "order":
@@ -687,14 +705,14 @@ def test_bad_lists_are_errors(spr, gpu):
             O, _ = s.attend(sel, cnt)
             assert spr.sparsepr_paged_error(s.ws) == 1, what
             assert torch.equal(O[:new[0]], good[:new[0]])
-            assert torch.isnan(O[new[0]:]).all(), what
+            assert torch.isnan(O[new[0]:sum(new)]).all(), what
 
 
 # ---------------------------------------------------------------------------
 # A run of them together
 # ---------------------------------------------------------------------------
-@pytest.mark.parametrize("dt,sparse", [(BF, False), (FP, True)])
-def test_rollout(spr, gpu, dt, sparse):
+@pytest.mark.parametrize("dt,sparse,wide", [(BF, False, 0), (BF, False, 450), (FP, True, 0)])
+def test_rollout(spr, gpu, dt, sparse, wide):
     """Three frames generated one after another, then single tokens: rotation, append, selection
     and attention through rollout_step, against attention over everything so far in 64 bits."""
     B, Hq, Hkv, d, page, F = 2, 4, 2, 64, 32, 48
@@ -703,12 +721,14 @@ def test_rollout(spr, gpu, dt, sparse):
     q, k, v = (torch.randn(B, total, h, d, generator=g).to(dt) for h in (Hq, Hkv, Hkv))
     npg = -(-total // page)
     table = torch.randperm(B * npg + 1, generator=g)[:B * npg].reshape(B, npg).to(torch.int32)
+    if wide:      # a page table for much longer sequences: the frames go to the tensor tiles
+        table = torch.cat([table, torch.full((B, wide - npg), 2 ** 31 - 1, dtype=torch.int32)], 1)
     cache = None
     fr = R.rope_freqs([24, 20, 20])
     grid = torch.stack([torch.arange(total) // F, torch.arange(total) % F // 8, torch.arange(total) % 8]).to(torch.int32)
     at = 0
     for n in (F, F, F, 1, 1, 1):
-        p = spr.CacheParams.make(B, Hq, Hkv, d, dtype=dt, page=page, n_pages=B * npg + 1, max_pages=npg, T=B * n, max_chunk=n,
+        p = spr.CacheParams.make(B, Hq, Hkv, d, dtype=dt, page=page, n_pages=B * npg + 1, max_pages=wide or npg, T=B * n, max_chunk=n,
                                  frame=F, q_block=16 if sparse else 0, n_select=3 if sparse else 0, n_recent=1 if sparse else 0)
         if cache is None:
             cache = spr.alloc_cache(p, gpu)
@@ -753,7 +773,8 @@ def test_rollout(spr, gpu, dt, sparse):
                     assert torch.all((O[b * n + i, h].cpu().double() - ref).abs() <= tol)
 
 
-def test_agrees_with_the_dense_frame_causal_call(spr, gpu):
+@pytest.mark.parametrize("wide", [False, True])
+def test_agrees_with_the_dense_frame_causal_call(spr, gpu, wide):
     """The last frame of a frame-causal dense call equals the chunk over the cache of all frames."""
     H, d, F, frames, page = 2, 64, 96, 3, 32
     N = F * frames
@@ -764,16 +785,19 @@ def test_agrees_with_the_dense_frame_causal_call(spr, gpu):
                          sub_rank=8, kmeans_iters=1, frame_id=fid, n_frames=frames)
     O, lse = torch.empty_like(Q), torch.empty(H, N, device=gpu)
     spr.sparsepr_dense_attention(dp, Q, K, V, O, lse, torch.zeros(512, dtype=torch.uint8, device=gpu))
-    p = spr.CacheParams.make(1, H, H, d, page=page, n_pages=N // page, max_pages=N // page, T=F, max_chunk=F, frame=F)
+    mp = 900 if wide else N // page         # wide: to the tensor tiles
+    p = spr.CacheParams.make(1, H, H, d, page=page, n_pages=N // page, max_pages=mp, T=F, max_chunk=F, frame=F)
     order = torch.randperm(N // page, generator=g).to(gpu)
     pages = {n: torch.empty(N // page, H, page, d, dtype=BF, device=gpu) for n in "kv"}
     for n, t in (("k", K), ("v", V)):
         pages[n][order] = t[0].reshape(H, N // page, page, d).transpose(0, 1)
     ws = spr.paged_workspace(p, gpu)
+    table = torch.zeros(1, mp, dtype=torch.int32, device=gpu)
+    table[0, :N // page] = order
     q = Q[0, :, N - F:].transpose(0, 1)
     o, z = torch.empty(F, H, d, dtype=BF, device=gpu), torch.empty(F, H, device=gpu)
     spr.sparsepr_paged_attention(p, q, torch.tensor([0, F], dtype=torch.int32, device=gpu),
-                                 torch.tensor([N], dtype=torch.int32, device=gpu), order.to(torch.int32)[None].contiguous(),
+                                 torch.tensor([N], dtype=torch.int32, device=gpu), table,
                                  pages["k"], pages["v"], o, z, ws)
     want = O[0, :, N - F:].transpose(0, 1).float()
     # each side within u |o| + u A of the exact value, A <= max |v| < 5
@@ -782,9 +806,11 @@ def test_agrees_with_the_dense_frame_causal_call(spr, gpu):
 
 
 def test_graphs_and_streams(spr, gpu):
-    """Captured steps replay on new inputs; two graphs with a workspace each run at once."""
+    """Captured steps replay on new inputs; graphs with a workspace each run at once."""
     scenes = [Scene(spr, gpu, [1, 1], [900, 400], Hq=4, Hkv=2, d=64, page=16, dt=BF, q_block=1, n_select=8, n_recent=2, seed=41),
-              Scene(spr, gpu, [40], [700], Hq=2, Hkv=1, d=64, page=32, dt=BF, q_block=40, n_select=8, n_recent=2, seed=42)]
+              Scene(spr, gpu, [40], [700], Hq=2, Hkv=1, d=64, page=32, dt=BF, q_block=40, n_select=8, n_recent=2, seed=42),
+              Scene(spr, gpu, [40], [700], Hq=2, Hkv=1, d=64, page=32, dt=BF, q_block=40, n_select=8, n_recent=2, seed=44,
+                    tiles=True)]
     graphs = []
     for s in scenes:
         sel, cnt = spr.alloc_selection(s.p, gpu)
@@ -808,12 +834,13 @@ def test_graphs_and_streams(spr, gpu):
         for s, (gph, step, O, z) in zip(scenes, graphs):
             s.dev["Q"].copy_(torch.randn(s.Q.shape, generator=gen(50 + i)).to(BF))
             O.fill_(9.0)
+            z.fill_(9.0)
             step()
             want.append((O.clone(), z.clone()))
             O.fill_(9.0)
             z.fill_(9.0)
         torch.cuda.synchronize()
-        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        streams = [torch.cuda.Stream() for _ in graphs]
         for _ in range(5):
             for st, (gph, *_r) in zip(streams, graphs):
                 with torch.cuda.stream(st):
@@ -826,8 +853,8 @@ def test_graphs_and_streams(spr, gpu):
 
 
 def test_repeat_is_bitwise_equal(spr, gpu):
-    for new, kv in (([1], [9000]), ([60], [3000])):
-        s = Scene(spr, gpu, new, kv, Hq=4, Hkv=1, d=128, page=64, dt=BF, seed=61)
+    for new, kv, tiles in (([1], [9000], False), ([60], [3000], False), ([60], [3000], True)):
+        s = Scene(spr, gpu, new, kv, Hq=4, Hkv=1, d=128, page=64, dt=BF, seed=61, tiles=tiles)
         O, z = s.attend()
         for _ in range(5):
             O2, z2 = s.attend()
