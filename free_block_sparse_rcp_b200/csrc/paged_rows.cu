@@ -2,7 +2,8 @@
 // of split items.
 //
 // An item is the new tokens of one sequence (or of one unit with its page list) and the query
-// heads of one key/value head: at most 32 rows, which share one stream of keys.  The work is
+// heads of one key/value head, or 32 rows of them in a small call: at most 32 rows, which share one
+// stream of keys.  The work is
 // reading that stream: 4 d bytes per key for 4 d rows operations, so the kernel is built to
 // keep memory busy and uses the small warp-wide matrix product (16 x 8 x 16); a 128-row
 // tensor-core tile would be mostly padding here.
