@@ -685,7 +685,8 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int
                      bool sel) {
   PagedPlan p{};
   const long long G = Hq / Hkv;
-  const long long tok = sel && q_block < max_chunk ? q_block : max_chunk;
+  const int most_new = max_chunk < T ? max_chunk : T;
+  const long long tok = sel && q_block < most_new ? q_block : most_new;
   const long long rows = tok * G;
   const long long pairs = (long long)T * Hq * ((sel ? n_select : max_pages) * (long long)page);
   p.rows = rows <= 32 || pairs <= (sel ? 2000000 : 5000000);

@@ -708,6 +708,21 @@ def test_bad_lists_are_errors(spr, gpu):
             assert torch.isnan(O[new[0]:sum(new)]).all(), what
 
 
+@pytest.mark.parametrize("Hq", [2, 40])
+def test_limits_beyond_the_rows_of_the_call(spr, gpu, Hq):
+    """A max_chunk and a q_block that no sequence can reach count as T."""
+    kw = dict(Hq=Hq, Hkv=1, d=64, page=16, dt=BF, n_select=6, n_recent=1, seed=27)
+    s = Scene(spr, gpu, [30], [500], q_block=30, **kw)
+    t = Scene(spr, gpu, [30], [500], q_block=2 ** 31 - 1, max_chunk=2 ** 31 - 1, **kw)
+    O, z = s.attend()
+    s.check(O, z)
+    P, y = t.attend()
+    assert torch.equal(O, P) and torch.equal(z, y)
+    O, z = s.attend(*s.select())
+    P, y = t.attend(*t.select())
+    assert torch.equal(O, P) and torch.equal(z, y) and spr.sparsepr_paged_error(t.ws) == 0
+
+
 # ---------------------------------------------------------------------------
 # A run of them together
 # ---------------------------------------------------------------------------

@@ -152,6 +152,18 @@ def test_workspace_holds_the_pieces(spr):
     assert sel >= plain + 2 * 4000 * 4
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(n_select=4, q_block=40), dict(Hq=4096, Hkv=1, n_select=4, q_block=40)])
+def test_limits_beyond_the_rows_of_the_call(spr, kw):
+    """A max_chunk or q_block that no sequence can reach counts as T: same plan, same workspace."""
+    big = dict(kw, max_chunk=2 ** 31 - 1)
+    if "q_block" in kw:
+        big["q_block"] = 2 ** 31 - 1
+    same = dict(kw, max_chunk=40)
+    for T in (1, 40):
+        want = spr.sparsepr_paged_workspace_bytes(_cache(spr, **dict(same, T=T, B=1)))
+        assert 0 < want == spr.sparsepr_paged_workspace_bytes(_cache(spr, **dict(big, T=T, B=1)))
+
+
 def test_calls_refuse_before_cuda(spr):
     lib = spr._lib
     ok = ctypes.c_void_p(1 << 20)       # never dereferenced
