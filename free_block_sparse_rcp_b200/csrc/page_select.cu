@@ -21,10 +21,15 @@
 // few units; the selection then runs as a second kernel over the stored scores, which finds its unit
 // and mean query while the scores are made (5 units of a 475-token call over 36,000 keys, with their
 // attention: 34.5 us, 39.6 without).
-// Measured: 32 units of 64 tokens x 8 heads over 1,024 pages (d 128) 25 us: finding
-// the unit 1.8, the mean query 5, the scores 11 (each unit reads its head's means: 64 MB from L2 at
-// 6 TB/s), the list 7.  Half the instructions per score took the same time.
+// Several units of one sequence read the same means: with four or more of them per sequence their
+// mean queries come from a kernel of their own, and a block scores four units with each mean that it
+// reads.  One list per block reads its head's means from L2 for itself (256 lists of 1,024 pages: 64 MB
+// at 6 TB/s, 11 of 25 us, and half the instructions per score took the same time).  With the
+// attention over the lists: 2,048 tokens in units of 64, 8 heads, 1,024 pages 188 -> 180 us; 2,083
+// in units of 16, 4 heads, 1,140 pages 120 -> 100 us; 2,113 in units of 128, 4 heads, 1,530 pages
+// 65 -> 58 us; fewer than 64 lists leave the GPU empty in three kernels instead of one.
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace spr {
 namespace {
@@ -35,6 +40,8 @@ constexpr int kSelThreads = 512;
 constexpr int kSelBins = 2048;
 constexpr int kSelSmemPages = 8192;   // scores and keys in shared memory up to this many pages (96 KB)
 constexpr int kSelExact = 64;         // pages scored again in one step
+constexpr int kSelGroup = 4;          // units that k_group_score scores together
+constexpr double kSelTiny = 7.8886090522101181e-31;   // 2^-100
 
 // largest exponent field of a packed pair's halves, as a bit pattern: >= kInf: not finite
 template <typename T>
@@ -71,8 +78,9 @@ struct UnitInfo {
   int b, len, ntok, tok0, vis;   // tok0: packed row of the unit's first token; vis: visible pages
 };
 
+template <int NT>
 __device__ __forceinline__ bool unit_of(const SelectArgs& a, int idx, int* sm, UnitInfo& u) {
-  const paged::Found f = paged::find_item<paged::kUnits, kSelThreads>(a.p, idx, 1, 1, sm);
+  const paged::Found f = paged::find_item<paged::kUnits, NT>(a.p, idx, 1, 1, sm);
   if (f.b < 0) return false;
   const paged::Seq s = paged::make_seq(a.p, f.b, f.lo, f.hi, f.len);
   if (s.bad && threadIdx.x == 0) set_error(a.p.err, DERR_INDEX);
@@ -351,10 +359,10 @@ __device__ void pick_list(const SelectArgs& a, const UnitInfo& u, int h, const u
 }
 
 // The unit's mean query in 64 bits (NaN throughout if a query element is not finite).
-template <typename T, int D>
+template <typename T, int D, int NT>
 __device__ void mean_query(const SelectArgs& a, const UnitInfo& u, int h, double* q /* [D] */,
-                           double (*red)[D + 1] /* [kSelThreads / (D / 8)] */) {
-  constexpr int CH = D / 8, RG = kSelThreads / CH, UQ = 4;   // chunks of a row, rows per pass, passes in flight
+                           double (*red)[D + 1] /* [NT / (D / 8)] */) {
+  constexpr int CH = D / 8, RG = NT / CH, UQ = 4;   // chunks of a row, rows per pass, passes in flight
   const int tid = threadIdx.x, c = tid % CH, g0 = tid / CH, G = a.p.G, rows = u.ntok * G;
   if (g0 < rows) {
     double s[8] = {0., 0., 0., 0., 0., 0., 0., 0.};
@@ -408,11 +416,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_page_score(SelectArgs a) {
   const int tid = threadIdx.x, h = blockIdx.y;
   const int unit = blockIdx.x / a.splits, split = blockIdx.x - unit * a.splits;
   UnitInfo u;
-  if (!unit_of(a, unit, sm_find, u)) return;
+  if (!unit_of<kSelThreads>(a, unit, sm_find, u)) return;
   int* hist = reinterpret_cast<int*>(sm_sel);
   // the reduction of the mean query and, later, the keys share the space behind the bins
   unsigned char* rest = sm_sel + kSelBins * 4;
-  mean_query<T, D>(a, u, h, s_q, reinterpret_cast<double(*)[D + 1]>(rest));
+  mean_query<T, D, kSelThreads>(a, u, h, s_q, reinterpret_cast<double(*)[D + 1]>(rest));
   const size_t list = (size_t)unit * a.p.Hkv + h;
   const bool stored = a.splits > 1 || a.keys_global;
   uint32_t* keys = stored ? reinterpret_cast<uint32_t*>(a.scores) + list * a.p.max_pages
@@ -429,7 +437,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_page_score(SelectArgs a) {
     const double v = s_q[(i / 8) * 64 + sub * 8 + (i & 7)];
     q[i] = (float)v;
     nan |= !(v == v);
-    tiny |= v != 0. && fabs(v) < 7.8886090522101181e-31;    // 2^-100
+    tiny |= v != 0. && fabs(v) < kSelTiny;
   }
   nan = __any_sync(0xffffffffu, nan);
   tiny = __any_sync(0xffffffffu, tiny);
@@ -503,22 +511,250 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_page_score(SelectArgs a) {
                   a.sel + list * a.p.n_select, a.cnt + list);
 }
 
-// grid (units, Hkv): the lists from stored scores
+// ---------------------------------------------------------------------------
+// Several units of a sequence: k_unit_mean (mean queries), k_group_score (each page's mean serves four
+// units), k_page_pick.
+// ---------------------------------------------------------------------------
+constexpr int kGroupThreads = 256;
+
+// grid (units, Hkv)
 template <typename T, int D>
+__global__ void __launch_bounds__(kGroupThreads) k_unit_mean(SelectArgs a) {
+  __shared__ double red[kGroupThreads / (D / 8)][D + 1];
+  __shared__ int sm_find[kGroupThreads / 32 + 8];
+  __shared__ double s_q[D];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int unit = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  UnitInfo u;
+  const bool any = unit_of<kGroupThreads>(a, unit, sm_find, u);
+  if (h == 0 && tid == 0) a.info[unit] = any ? make_int2(u.b, u.vis) : make_int2(-1, 0);
+  if (!any) return;
+  mean_query<T, D, kGroupThreads>(a, u, h, s_q, red);
+  if (tid < D) a.qbar[((size_t)unit * a.p.Hkv + h) * D + tid] = s_q[tid];
+}
+
+// grid (groups of four units x splits, Hkv): the scores of the split's share of the pages.  The units
+// of a group that belong to one sequence are scored together.
+template <typename T, int D>
+__global__ void __launch_bounds__(kGroupThreads, 2) k_group_score(SelectArgs a) {
+  constexpr int U = kSelGroup, CPL = D / 8, NP = CPL / 2;     // columns of a lane, as pairs
+  constexpr int PPB = kGroupThreads / 8, UN = 4;              // pages of the block per step, steps in flight
+  __shared__ uint64_t s_q2[NP][U][8];
+  __shared__ double s_qq[U];
+  __shared__ int s_nan[U], s_wide[U];
+  __shared__ int2 s_info[U];
+  __shared__ float s_kk[kGroupThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = tid & 7, h = blockIdx.y;
+  const int group = blockIdx.x / a.splits, split = blockIdx.x - group * a.splits, u0 = group * U;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the mean queries are complete
+  if (warp < U) {
+    const int unit = u0 + warp;
+    const int2 info = unit < a.units ? a.info[unit] : make_int2(-1, 0);
+    double qq = 0.;
+    bool nan = false, tiny = false;
+    for (int i = lane; i < D / 2; i += 32) {      // pair i: columns 2 i, 2 i + 1
+      double2 v = make_double2(0., 0.);
+      if (info.x >= 0) v = *reinterpret_cast<const double2*>(a.qbar + ((size_t)unit * a.p.Hkv + h) * D + 2 * i);
+      const int c = i / 32, l = (i & 31) >> 2, p = i & 3;     // column 2 i = 64 c + 8 l + 2 p
+      s_q2[c * 4 + p][warp][l] = tc::f2pack((float)v.x, (float)v.y);
+      qq = fma(v.x, v.x, fma(v.y, v.y, qq));
+      nan |= !(v.x == v.x) || !(v.y == v.y);
+      tiny |= (v.x != 0. && fabs(v.x) < kSelTiny) || (v.y != 0. && fabs(v.y) < kSelTiny);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) qq += __shfl_xor_sync(0xffffffffu, qq, o);
+    nan = __any_sync(0xffffffffu, nan);
+    tiny = __any_sync(0xffffffffu, tiny);
+    if (lane == 0) {
+      s_info[warp] = info;
+      s_qq[warp] = qq;
+      s_nan[warp] = nan;
+      s_wide[warp] = tiny;
+    }
+  }
+  __syncthreads();
+  // this lane's results: page sub / 2 of the step's four, units 2 (sub & 1) and the next
+  const int mp = sub >> 1, mu = 2 * (sub & 1);
+  for (int r0 = 0; r0 < U;) {
+    const int b = s_info[r0].x;
+    int r1 = r0, vis = 0;
+    for (; r1 < U && s_info[r1].x == b; ++r1) vis = max(vis, s_info[r1].y);
+    if (b < 0) {
+      r0 = r1;
+      continue;
+    }
+    const int p0 = (int)((long long)vis * split / a.splits), p1 = (int)((long long)vis * (split + 1) / a.splits);
+    const int* table = a.p.table + (size_t)b * a.p.max_pages;
+    bool mine[2], nanu[2];
+    int visu[2];
+    uint32_t* keys[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int u = mu + k;
+      mine[k] = u >= r0 && u < r1;
+      nanu[k] = s_nan[u] != 0;
+      visu[k] = s_info[u].y;
+      keys[k] = reinterpret_cast<uint32_t*>(a.scores) + ((size_t)(u0 + u) * a.p.Hkv + h) * a.p.max_pages;
+    }
+    bool wide[2] = {false, false}, wide_all = false;
+    float kk = 0.f;                  // largest sum of squares of this lane's columns of a page
+    int id[UN];
+#pragma unroll
+    for (int s = 0; s < UN; ++s) id[s] = p0 + s * PPB + (tid >> 3) < p1 ? table[p0 + s * PPB + (tid >> 3)] : -2;
+    for (int j0 = p0; j0 < p1; j0 += PPB * UN) {
+      uint4 w[UN][CPL / 8];
+      bool ok[UN];
+#pragma unroll
+      for (int s = 0; s < UN; ++s) {
+        ok[s] = id[s] >= 0 && id[s] < a.p.n_pages;
+        if (!ok[s] && id[s] != -2 && sub == 0) set_error(a.p.err, DERR_INDEX);
+        const T* row = (const T*)a.km + ((size_t)(ok[s] ? id[s] : 0) * a.p.Hkv + h) * D;
+#pragma unroll
+        for (int c = 0; c < CPL / 8; ++c) w[s][c] = *reinterpret_cast<const uint4*>(row + c * 64 + sub * 8);
+      }
+      // the next step's ids
+#pragma unroll
+      for (int s = 0; s < UN; ++s) {
+        const int j = j0 + (UN + s) * PPB + (tid >> 3);
+        id[s] = j < p1 ? table[j] : -2;
+      }
+      uint64_t x2[UN][U], k2[UN];
+#pragma unroll
+      for (int s = 0; s < UN; ++s) {
+        k2[s] = 0ull;
+#pragma unroll
+        for (int u = 0; u < U; ++u) x2[s][u] = 0ull;
+      }
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        uint64_t q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = s_q2[i][u][sub];
+#pragma unroll
+        for (int s = 0; s < UN; ++s) {
+          const uint4 v = w[s][i >> 2];
+          const float2 f = unpack2<T>((i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w);
+          const uint64_t f2 = tc::f2pack(f.x, f.y);
+          k2[s] = tc::ffma2(f2, f2, k2[s]);
+#pragma unroll
+          for (int u = 0; u < U; ++u) x2[s][u] = tc::ffma2(f2, q[u], x2[s][u]);
+        }
+      }
+      // sums over the eight lanes, each lane left with two of the sixteen
+      float v[UN * U];
+#pragma unroll
+      for (int s = 0; s < UN; ++s)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float x0, x1;
+          tc::f2unpack(x2[s][u], x0, x1);
+          v[s * U + u] = x0 + x1;
+        }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        const bool hi = (sub & o) != 0;
+#pragma unroll
+        for (int i = 0; i < 2 * o; ++i) {
+          const float send = hi ? v[i] : v[i + 2 * o], keep = hi ? v[i + 2 * o] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+      bool odd = false;                // something that is not finite among these pages
+      bool okm = false;
+#pragma unroll
+      for (int s = 0; s < UN; ++s) {
+        float k0, k1;
+        tc::f2unpack(k2[s], k0, k1);
+        const float ks = k0 + k1;
+        if (ok[s]) {
+          if (ks < INFINITY) kk = fmaxf(kk, ks);
+          else odd = true;
+        }
+        if (s == mp) okm = ok[s];
+      }
+      bool over[2], fin = true;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        over[k] = !(fabsf(v[k]) < INFINITY);
+        odd |= over[k] && okm && mine[k] && !nanu[k];
+      }
+      // An infinity or a NaN among the means shows in the score or in the sum of squares; only then
+      // are the elements looked at, since a finite page's sums may overflow 32 bits.
+      if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+        for (int s = 0; s < UN; ++s) {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int c = 0; c < CPL / 8; ++c) {
+            const uint32_t p[4] = {w[s][c].x, w[s][c].y, w[s][c].z, w[s][c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max_abs2(m, p[i]);
+          }
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const bool f = finite2<T>(m);
+          float k0, k1;
+          tc::f2unpack(k2[s], k0, k1);
+          if (ok[s] && f && !(k0 + k1 < INFINITY)) wide_all = true;
+          if (s == mp) fin = f;
+        }
+      }
+      const int j = j0 + mp * PPB + (tid >> 3);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (!mine[k] || j >= p1 || j >= visu[k]) continue;
+        const bool scored = okm && fin && !nanu[k];
+        // a finite page whose score overflows is decided in 64 bits, and all others with it
+        wide[k] |= scored && over[k];
+        keys[k][j] = !scored ? 0u : (over[k] ? 1u : order32(v[k]));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (wide[k]) s_wide[mu + k] = 1;
+    if (wide_all)
+      for (int u = r0; u < r1; ++u) s_wide[u] = 1;
+#pragma unroll
+    for (int o = 16; o > 4; o >>= 1) kk = fmaxf(kk, __shfl_xor_sync(0xffffffffu, kk, o));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) kk += __shfl_xor_sync(0xffffffffu, kk, o);
+    if (lane == 0) s_kk[warp] = kk;
+    __syncthreads();
+    if (tid >= r0 && tid < r1) {
+      float most = 0.f;
+      for (int w = 0; w < kGroupThreads / 32; ++w) most = fmaxf(most, s_kk[w]);
+      const float eps = (float)sqrt(s_qq[tid] * ((double)most + 7.2e-43));     // products below fp32's range: 2^-140
+      a.bounds[((size_t)(u0 + tid) * a.p.Hkv + h) * a.splits + split] = s_wide[tid] || !(eps < INFINITY) ? INFINITY : eps;
+    }
+    __syncthreads();
+    r0 = r1;
+  }
+}
+
+// grid (units, Hkv): the lists from stored scores (GROUP: those of k_group_score)
+template <typename T, int D, bool GROUP>
 __global__ void __launch_bounds__(kSelThreads) k_page_pick(SelectArgs a) {
   extern __shared__ __align__(16) unsigned char sm_sel[];
   __shared__ int sm_find[kSelThreads / 32 + 8];
   __shared__ double s_q[D];
   const int unit = blockIdx.x, h = blockIdx.y;
   UnitInfo u;
-  if (!unit_of(a, unit, sm_find, u)) {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    return;
-  }
   int* hist = reinterpret_cast<int*>(sm_sel);
   unsigned char* rest = sm_sel + kSelBins * 4;
-  mean_query<T, D>(a, u, h, s_q, reinterpret_cast<double(*)[D + 1]>(rest));
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the scores are complete
+  if (GROUP) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the scores are complete
+    const int2 info = a.info[unit];
+    if (info.x < 0) return;
+    u.b = info.x;
+    u.vis = info.y;
+    if (threadIdx.x < D) s_q[threadIdx.x] = a.qbar[((size_t)unit * a.p.Hkv + h) * D + threadIdx.x];
+  } else {
+    const bool any = unit_of<kSelThreads>(a, unit, sm_find, u);
+    if (any) mean_query<T, D, kSelThreads>(a, u, h, s_q, reinterpret_cast<double(*)[D + 1]>(rest));
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the scores are complete
+    if (!any) return;
+  }
   const size_t list = (size_t)unit * a.p.Hkv + h;
   const uint32_t* keys = reinterpret_cast<const uint32_t*>(a.scores) + list * a.p.max_pages;
   unsigned long long* keys64 = a.keys + list * a.p.max_pages;
@@ -540,18 +776,28 @@ cudaError_t launch_select_t(const SelectArgs& a, int* launches, cudaStream_t st)
   const size_t keys = (((size_t)a.p.max_pages * 4 + 15) & ~(size_t)15) + (size_t)a.p.max_pages * 8;
   const bool stored = a.splits > 1 || a.keys_global;
   const size_t all = kSelBins * 4 + (a.keys_global || keys < red ? red : keys), score = kSelBins * 4 + (stored ? red : all - kSelBins * 4);
-  cudaError_t e = cudaFuncSetAttribute(k_page_score<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)score);
+  cudaError_t e;
+  auto pick = [&](auto kern) -> cudaError_t {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
+    if (err != cudaSuccess) return err;
+    ++*launches;
+    return launch_early(kern, dim3((unsigned)a.units, a.p.Hkv), kSelThreads, all, st, a);
+  };
+  *launches = 0;
+  if (a.group) {
+    k_unit_mean<T, D><<<dim3((unsigned)a.units, a.p.Hkv), kGroupThreads, 0, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const unsigned groups = (unsigned)((a.units - 1) / kSelGroup + 1);
+    if ((e = launch_early(k_group_score<T, D>, dim3(groups * a.splits, a.p.Hkv), kGroupThreads, 0, st, a)) != cudaSuccess) return e;
+    *launches = 2;
+    return pick(k_page_pick<T, D, true>);
+  }
+  e = cudaFuncSetAttribute(k_page_score<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)score);
   if (e != cudaSuccess) return e;
   k_page_score<T, D><<<dim3((unsigned)a.units * a.splits, a.p.Hkv), kSelThreads, score, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   *launches = 1;
-  if (stored) {
-    e = cudaFuncSetAttribute(k_page_pick<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
-    if (e != cudaSuccess) return e;
-    e = launch_early(k_page_pick<T, D>, dim3((unsigned)a.units, a.p.Hkv), kSelThreads, all, st, a);
-    *launches = 2;
-  }
-  return e;
+  return stored ? pick(k_page_pick<T, D, false>) : cudaSuccess;
 }
 
 template <typename T>
@@ -561,11 +807,17 @@ cudaError_t launch_select_d(const SelectArgs& a, int d, int* launches, cudaStrea
 
 }  // namespace
 
-// Splits of a unit's pages: enough blocks for two per SM, at least 256 pages each (one step of a
-// block).
-SelectPlan select_plan(int units, int Hkv, int max_pages) {
-  SelectPlan p{1, max_pages > kSelSmemPages};
+// Splits of a unit's (or group's) pages: enough blocks for two per SM, at least 256 pages each.
+SelectPlan select_plan(int units, int Hkv, int max_pages, int B) {
+  SelectPlan p{1, max_pages > kSelSmemPages, false};
   const long long blocks = (long long)units * Hkv;
+  if (units >= kSelGroup * (long long)B && blocks >= 64) {     // groups of mostly one sequence
+    p.group = true;
+    const long long groups = ceil_div64(units, kSelGroup) * (long long)Hkv, most = ceil_div(max_pages, 256);
+    const long long s = 296 / groups < most ? 296 / groups : most;
+    p.splits = s < 1 ? 1 : (int)s;
+    return p;
+  }
   if (blocks > 0 && blocks < 148) {
     long long s = 296 / blocks;
     const long long most = ceil_div(max_pages, 256);

@@ -311,16 +311,19 @@ struct SelectArgs {
   int* sel;
   int* cnt;
   float* scores;                  // [units][Hkv][max_pages] and
-  float* bounds;                  // [units][Hkv][splits], used with splits > 1
+  float* bounds;                  // [units][Hkv][splits], used with splits > 1 or `group`
   unsigned long long* keys;       // [units][Hkv][max_pages], used when `keys_global`
+  double* qbar;                   // [units][Hkv][d] and
+  int2* info;                     // [units] sequence and visible pages, used when `group`
   int n_sink, n_recent, units, splits;
-  bool keys_global;
+  bool keys_global, group;
 };
 struct SelectPlan {
   int splits;
   bool keys_global;
+  bool group;       // four units' scores together
 };
-SelectPlan select_plan(int units, int Hkv, int max_pages);
+SelectPlan select_plan(int units, int Hkv, int max_pages, int B);
 cudaError_t launch_page_select(const SelectArgs& a, int d, int dtype, int* launches, cudaStream_t st);
 
 // rows kernel: items of at most 16 * mt query rows on mma.sync; tile kernel: 256-row items on

@@ -210,7 +210,7 @@ int select_units(const sparsepr_cache_params& p) {
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Layout {
-  size_t part_lse, part_o, plan, plan_seq, plan_item, plan_pre, scores, bounds, keys, total;
+  size_t part_lse, part_o, plan, plan_seq, plan_item, plan_pre, scores, bounds, keys, qbar, info, total;
 };
 Layout layout_of(const sparsepr_cache_params& p) {
   Layout L{};
@@ -233,17 +233,23 @@ Layout layout_of(const sparsepr_cache_params& p) {
   L.plan_item = take(items * 4);
   L.plan_pre = take(items * p.Hkv * 8);
   // selection: scores of split lists, and 64-bit keys of lists too long for shared memory
-  size_t scores = 0, bounds = 0, keys = 0;
+  size_t scores = 0, bounds = 0, keys = 0, qbar = 0, info = 0;
   if (p.n_select > 0) {
     const size_t lists = (size_t)select_units(p) * p.Hkv;
-    const SelectPlan sp = select_plan(select_units(p), p.Hkv, p.max_pages);
-    if (sp.splits > 1 || sp.keys_global) scores = lists * p.max_pages * 4;
+    const SelectPlan sp = select_plan(select_units(p), p.Hkv, p.max_pages, p.B);
+    if (sp.splits > 1 || sp.keys_global || sp.group) scores = lists * p.max_pages * 4;
     bounds = lists * sp.splits * 4;
     if (sp.keys_global) keys = lists * p.max_pages * 8;
+    if (sp.group) {
+      qbar = lists * p.d * 8;
+      info = (size_t)select_units(p) * 8;
+    }
   }
   L.scores = take(scores);
   L.bounds = take(bounds);
   L.keys = take(keys);
+  L.qbar = take(qbar);
+  L.info = take(info);
   L.total = o;
   return L;
 }
@@ -378,9 +384,12 @@ sparsepr_status sparsepr_page_select(const sparsepr_cache_params* p, const void*
   a.keys = at<unsigned long long>(workspace, L.keys);
   a.n_sink = p->n_sink; a.n_recent = p->n_recent;
   a.units = select_units(*p);
-  const SelectPlan sp = select_plan(a.units, p->Hkv, p->max_pages);
+  const SelectPlan sp = select_plan(a.units, p->Hkv, p->max_pages, p->B);
   a.splits = sp.splits;
   a.keys_global = sp.keys_global;
+  a.group = sp.group;
+  a.qbar = at<double>(workspace, L.qbar);
+  a.info = at<int2>(workspace, L.info);
   int launches = 0;
   const cudaError_t e = launch_page_select(a, p->d, p->dtype, &launches, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "launch_page_select");

@@ -584,6 +584,8 @@ SELECT = [  # new, kv, Hq, Hkv, d, page, dtype, frame, q_block, n_select, n_sink
     ([300], [600], 4, 1, 64, 32, BF, 1, 100, 9, 1, 2),            # units of several row parts
     ([3, 3], [90, 200], 16, 1, 64, 16, BF, 1, 2, 4, 1, 1),        # 32 rows per unit
     ([1, 3], [900, 64], 48, 1, 128, 16, FP, 1, 1, 6, 0, 1),       # a token's heads in two items
+    ([200, 0, 130], [1500, 10, 900], 8, 4, 128, 64, BF, 1, 4, 6, 1, 1),     # units scored four at a time, across sequences
+    ([150, 9, 70], [700, 9, 800], 32, 16, 64, 16, FP, 25, 7, 9, 0, 2),
 ]
 
 
@@ -630,14 +632,15 @@ def test_select_ties_and_nan(spr, gpu):
     assert 8 not in sel[0, 0].tolist() and cnt.item() == 399
 
 
+@pytest.mark.parametrize("units", [1, 42])       # 42: scored four at a time
 @pytest.mark.parametrize("n_pages", [300, 3000])
 @pytest.mark.parametrize("kind", ["near", "tied", "tiny", "huge", "inf_query", "inf_mean"])
-def test_select_scores_that_32_bits_cannot_order(spr, gpu, kind, n_pages):
+def test_select_scores_that_32_bits_cannot_order(spr, gpu, kind, n_pages, units):
     """Scores closer than the 32-bit sums are exact, hundreds of equal ones, values at the ends of
     the range, and infinities: the lists are still those of the 64-bit scores."""
     d, page = 64, 16
     g = gen(26)
-    s = Scene(spr, gpu, [1], [16 * n_pages], Hq=2, Hkv=2, d=d, page=page, dt=BF, q_block=1, n_select=57, n_sink=1, n_recent=1, seed=27)
+    s = Scene(spr, gpu, [units], [16 * n_pages], Hq=2, Hkv=2, d=d, page=page, dt=BF, q_block=1, n_select=57, n_sink=1, n_recent=1, seed=27)
     base = torch.randn(2, d, generator=g)
     km = base.expand(s.n_pages, 2, d).clone()
     if kind == "near":        # one small element tells the pages apart
@@ -665,23 +668,24 @@ def test_select_scores_that_32_bits_cannot_order(spr, gpu, kind, n_pages):
     assert torch.equal(cnt.cpu(), wc) and torch.equal(sel.cpu(), want)
 
 
-@pytest.mark.parametrize("Hkv", [1, 160])
-def test_select_many_pages(spr, gpu, Hkv):
-    """More pages than shared memory holds (scores in the workspace), one block per list or several."""
+@pytest.mark.parametrize("Hkv,T", [(1, 1), (160, 1), (16, 4)])
+def test_select_many_pages(spr, gpu, Hkv, T):
+    """More pages than shared memory holds (scores in the workspace), one block per list or several,
+    and units scored together."""
     page, d, npg = 16, 64, 9000
     g = gen(24)
     km = torch.randn(64, Hkv, d, generator=g).to(BF)
     table = torch.randint(0, 64, (1, npg), generator=g).to(torch.int32)     # pages used many times: ties
-    p = spr.CacheParams.make(1, Hkv, Hkv, d, page=page, n_pages=64, max_pages=npg, T=1, max_chunk=1, q_block=1,
+    p = spr.CacheParams.make(1, Hkv, Hkv, d, page=page, n_pages=64, max_pages=npg, T=T, max_chunk=T, q_block=1,
                              n_select=700, n_sink=2, n_recent=5)
-    Q = torch.randn(1, Hkv, d, generator=g).to(BF)
+    Q = torch.randn(T, Hkv, d, generator=g).to(BF)
     ws = spr.paged_workspace(p, gpu)
     sel, cnt = spr.alloc_selection(p, gpu)
-    spr.sparsepr_page_select(p, Q.to(gpu), torch.tensor([0, 1], dtype=torch.int32, device=gpu),
+    spr.sparsepr_page_select(p, Q.to(gpu), torch.tensor([0, T], dtype=torch.int32, device=gpu),
                              torch.tensor([npg * page], dtype=torch.int32, device=gpu), table.to(gpu), km.to(gpu), sel, cnt, ws)
     for h in (0, Hkv - 1):
-        want, _ = R.select(Q[:, h:h + 1], [1], [npg * page], table, km[:, h:h + 1], page, 1, 1, 700, 2, 5)
-        assert torch.equal(sel[0, h].cpu(), want[0, 0])
+        want, _ = R.select(Q[:, h:h + 1], [T], [npg * page], table, km[:, h:h + 1], page, 1, 1, 700, 2, 5)
+        assert torch.equal(sel[:, h].cpu(), want[:, 0])
     assert torch.all(cnt == 700)
 
 
