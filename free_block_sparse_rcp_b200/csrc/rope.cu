@@ -5,8 +5,8 @@
 // the gradient is the same with -t.  Both kernels move every row once and are bound by
 // memory, so a thread keeps the sines and cosines of its pairs in registers, where they serve
 // the heads of the token.
-// Measured: 32,760 tokens x 80 heads of d 128, bf16 (1.34 GB) 205 us, 6.5 TB/s, a copy's rate; 2 x
-// 5,003 tokens x 40 heads, fp32, half of d turned (410 MB) 75 us, 5.4 TB/s; 64 single tokens
+// Measured: 32,760 tokens x 80 heads of d 128, bf16 (1.34 GB) 210 us, 6.4 TB/s, a copy's rate; 2 x
+// 5,003 tokens x 40 heads, fp32, half of d turned (410 MB) 79 us, 5.2 TB/s; 64 single tokens
 // 3.8 us, the latency of one launch with a 64-bit product and a sine.
 // The turn count pos f is formed and reduced to [-1/2, 1/2] in 64 bits: in 32 bits the
 // angle of position 10^5 would be off by 2^-24 10^5 = 6e-3.
@@ -80,7 +80,9 @@ struct Vec {
 // How a row is divided among threads.
 //   kInter: one 16-byte chunk, holding whole pairs (pairs past rot/2 turn by 0)
 //   kHalf:  chunk c of the first half with chunk c of the second, then the copied chunks
-//   kPair:  one pair (or one copied element), for rows that 16-byte chunks do not fit
+//   kPair:  one pair, one copied element or (wide) one 16-byte chunk past the rotated part, for
+//           rotations that 16-byte chunks do not fit: 2 x 16 heads of 4,000 bf16 rows of d 128, of
+//           which 22 elements turn, take 20 us, 39 us with the copied elements one by one
 enum RopeMode { kInter = 0, kHalf = 1, kPair = 2 };
 
 template <typename T, int MODE>
@@ -88,10 +90,13 @@ struct RowUnits {
   static constexpr int E = Vec<T>::E;
   // pairs a unit turns, at most
   static constexpr int P = MODE == kInter ? E / 2 : (MODE == kHalf ? E : 1);
-  static __host__ __device__ int count(int d, int rot) {
+  // kPair: first element of the copied chunks
+  static __host__ __device__ int tail(int d, int rot, bool wide) { return wide ? (rot + E - 1) / E * E : d; }
+  static __host__ __device__ int count(int d, int rot, bool wide = false) {
     if (MODE == kInter) return d / E;
     if (MODE == kHalf) return rot / 2 / E + (d - rot) / E;
-    return rot / 2 + (d - rot);
+    const int t = tail(d, rot, wide);
+    return rot / 2 + (t - rot) + (d - t) / E;
   }
 };
 
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
   using U = RowUnits<T, MODE>;
   constexpr int E = U::E, P = U::P;
   const long long gid = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
-  const int upr = U::count(a.d, a.rot);
+  const int upr = U::count(a.d, a.rot, a.vec);
   if (gid >= units) return;
   const long long row = gid / upr;
   const int u = (int)(gid - row * upr);
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
   const int half = a.rot / 2;
   // first element, partner element (kHalf, kPair) and whether the unit turns
   int e0, e1 = 0, p0;
-  bool turns;
+  bool turns, wide = false;       // wide: a chunk of kPair
   if (MODE == kInter) {
     e0 = u * E;
     p0 = e0 / 2;
@@ -126,6 +131,12 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
     p0 = u;
     e0 = !turns ? a.rot + (u - half) : (a.layout == 0 ? u : 2 * u);
     e1 = a.layout == 0 ? e0 + half : e0 + 1;
+    const int tail = U::tail(a.d, a.rot, a.vec);
+    if (!turns && e0 >= tail) {
+      wide = true;
+      e0 = tail + (e0 - tail) * E;
+    }
+    if (!turns) e1 = e0;
   }
   float c[P], s[P];
   if (turns) {
@@ -186,19 +197,41 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
         *reinterpret_cast<uint4*>(y + h * yh + e1) = Vec<T>::pack(vb);
       }
     };
+    constexpr int UN = 4;   // heads in flight
     if (MODE == kPair) {
-      for (int h = first; h < a.H[t]; h += gy) {
-        if (!turns) {
-          y[h * yh + e0] = x[h * xh + e0];
+      for (int h0 = first; h0 < a.H[t]; h0 += UN * gy) {
+        if (wide) {
+          uint4 w[UN];
+#pragma unroll
+          for (int i = 0; i < UN; ++i)
+            if (h0 + i * gy < a.H[t]) Vec<T>::load(x + (h0 + i * gy) * xh + e0, w[i]);
+#pragma unroll
+          for (int i = 0; i < UN; ++i)
+            if (h0 + i * gy < a.H[t]) *reinterpret_cast<uint4*>(y + (h0 + i * gy) * yh + e0) = w[i];
           continue;
         }
-        const float p = as_f32(x[h * xh + e0]), q = as_f32(x[h * xh + e1]);
-        y[h * yh + e0] = from_f32<T>(p * c[0] - q * s[0]);
-        y[h * yh + e1] = from_f32<T>(p * s[0] + q * c[0]);
+        T p[UN], q[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i)
+          if (h0 + i * gy < a.H[t]) {
+            p[i] = x[(h0 + i * gy) * xh + e0];
+            q[i] = x[(h0 + i * gy) * xh + e1];
+          }
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+          if (h0 + i * gy >= a.H[t]) continue;
+          T* o = y + (h0 + i * gy) * yh;
+          if (turns) {
+            const float f = as_f32(p[i]), g = as_f32(q[i]);
+            o[e0] = from_f32<T>(f * c[0] - g * s[0]);
+            o[e1] = from_f32<T>(f * s[0] + g * c[0]);
+          } else {
+            o[e0] = p[i];
+          }
+        }
       }
       continue;
     }
-    constexpr int UN = 4;   // heads in flight
     auto batch = [&](int h0, auto whole) {
       uint4 wa[UN], wb[UN];
 #pragma unroll
@@ -220,7 +253,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
 
 template <typename T, int MODE>
 cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
-  const long long units = (long long)a.B * a.N * RowUnits<T, MODE>::count(a.d, a.rot);
+  const long long units = (long long)a.B * a.N * RowUnits<T, MODE>::count(a.d, a.rot, a.vec);
   const long long blocks = ceil_div64(units, kRopeThreads);
   const int heads = a.H[0] + a.H[1];
   // Heads are dealt to enough blocks to fill the GPU once (148 SMs x 4 blocks), and for large calls
@@ -279,12 +312,12 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int d = a.d, page = a.page, rot = ROPE ? a.rot : 0, half = rot / 2;
-  const int upr = U::count(d, rot);
+  const int upr = U::count(d, rot, true);      // the cache's rows are whole chunks
   const long long gid = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
   const int row = (int)min(gid / upr, (long long)a.T);       // a.T: past the last row
   const int u = (int)(gid - (long long)row * upr);
   int e0, e1 = 0, p0;
-  bool turns = false;
+  bool turns = false, wide = false;
   if (MODE == kInter) {
     e0 = u * E;
     p0 = e0 / 2;
@@ -299,6 +332,11 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
     p0 = u;
     e0 = !turns ? rot + (u - half) : (a.layout == 0 ? u : 2 * u);
     e1 = a.layout == 0 ? e0 + half : e0 + 1;
+    const int tail = U::tail(d, rot, true);
+    if (!turns && e0 >= tail) {
+      wide = true;
+      e0 = tail + (e0 - tail) * E;
+    }
   }
   // value chunks of the unit: u and u + upr, as far as the row has them (upr is at least half of
   // its chunks)
@@ -379,7 +417,9 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
       const int h = h0 + i * gy;
       if (h >= a.Hkv) continue;
       if (MODE == kPair) {
-        if (!turns) {
+        if (wide) {
+          *reinterpret_cast<uint4*>(kp + h * hstep + e0) = *reinterpret_cast<const uint4*>(K + h * a.ksh + e0);
+        } else if (!turns) {
           kp[h * hstep + e0] = K[h * a.ksh + e0];
         } else {
           const float p = as_f32(K[h * a.ksh + e0]), q = as_f32(K[h * a.ksh + e1]);
@@ -539,7 +579,7 @@ cudaError_t launch_means(const AppendArgs& a, cudaStream_t st) {
 
 template <typename T, int MODE, bool ROPE>
 cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t st) {
-  const long long units = (long long)a.T * RowUnits<T, MODE>::count(a.d, ROPE ? a.rot : 0);
+  const long long units = (long long)a.T * RowUnits<T, MODE>::count(a.d, ROPE ? a.rot : 0, true);
   const long long blocks = ceil_div64(units, kRopeThreads);
   // Heads are dealt to 256 blocks: 4 x 1,024 tokens of 16 heads take 19.0 us that way (8 heads per
   // thread), 21.3 us with 128 and 25.4 us with 1,024, where the angles serve two heads only.

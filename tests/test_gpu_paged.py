@@ -54,7 +54,10 @@ ROPE_CASES = [
     (1, 9, 0, 33, 64, 22, "half", [22], FP, "base", 2.0, 0),          # pairs that 16 bytes do not hold
     (1, 7, 4, 33, 64, 22, "interleaved", [22], BF, "base", 2.0, 0),   # the rotation ends inside a chunk
     (2, 3, 1, 11, 40, 38, "half", [2, 36], BF, "none", 1.0, 0),
+    (2, 19, 6, 23, 128, 22, "half", [10, 12], F32, "none", 1.0, 0),   # ... with chunks behind them
+    (1, 5, 2, 9, 40, 18, "half", [18], BF, "none", 1.0, 0),
     (1, 2, 1, 6, 6, 4, "interleaved", [4], FP, "none", 1.0, 0),       # rows of 12 bytes
+    (1, 2, 1, 6, 6, 4, "half", [4], FP, "none", 1.0, 0),
     (1, 2, 0, 6, 3, 2, "half", [2], F32, "none", 1.0, 0),
     (1, 1, 0, 2, 2, 2, "half", [2], BF, "none", 1.0, 0),
     (1, 3, 0, 9, 512, 512, "half", [512], FP, "none", 1.0, 0),
@@ -459,6 +462,7 @@ APPEND = [  # new, kv, Hkv, d, page, dtype, rope (rot, layout, axes) or None
     ([130, 65], [300, 65], 4, 128, 64, BF, (96, "half", [96])),
     ([129], [140], 1, 64, 128, FP, (22, "half", [22])),
     ([70], [150], 2, 128, 128, BF, (22, "interleaved", [22])),
+    ([70, 9], [150, 30], 5, 128, 64, BF, (22, "half", [10, 12])),
     ([50, 6], [20, 0], 2, 64, 16, BF, (64, "half", [64])),        # more new tokens than slots
     ([260], [260], 20, 64, 16, BF, (64, "half", [64])),           # several heads per block
 ]
