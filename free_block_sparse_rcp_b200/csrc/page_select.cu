@@ -41,6 +41,7 @@ constexpr int kSelBins = 2048;
 constexpr int kSelSmemPages = 8192;   // scores and keys in shared memory up to this many pages (96 KB)
 constexpr int kSelExact = 64;         // pages scored again in one step
 constexpr int kSelGroup = 4;          // units that k_group_score scores together
+constexpr long long kSelScores = 1 << 26;   // scores at most that are stored for it (256 MB)
 constexpr double kSelTiny = 7.8886090522101181e-31;   // 2^-100
 
 // largest exponent field of a packed pair's halves, as a bit pattern: >= kInf: not finite
@@ -811,7 +812,8 @@ cudaError_t launch_select_d(const SelectArgs& a, int d, int* launches, cudaStrea
 SelectPlan select_plan(int units, int Hkv, int max_pages, int B) {
   SelectPlan p{1, max_pages > kSelSmemPages, false};
   const long long blocks = (long long)units * Hkv;
-  if (units >= kSelGroup * (long long)B && blocks >= 64) {     // groups of mostly one sequence
+  // groups of mostly one sequence, and scores that a workspace may hold (4 bytes per list and page)
+  if (units >= kSelGroup * (long long)B && blocks >= 64 && blocks * max_pages <= kSelScores) {
     p.group = true;
     const long long groups = ceil_div64(units, kSelGroup) * (long long)Hkv, most = ceil_div(max_pages, 256);
     const long long s = 296 / groups < most ? 296 / groups : most;

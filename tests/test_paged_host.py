@@ -150,6 +150,11 @@ def test_workspace_holds_the_pieces(spr):
     sel = spr.sparsepr_paged_workspace_bytes(_cache(spr, B=1, T=1, max_chunk=1, max_pages=4000, n_pages=4000, n_select=8,
                                                     q_block=1))
     assert sel >= plain + 2 * 4000 * 4
+    # scores of units that share their pages' means are stored, but not without bound
+    chunk = dict(B=1, T=2048, max_chunk=2048, Hkv=8, n_select=64, max_pages=1024, n_pages=1024)
+    assert spr.sparsepr_paged_workspace_bytes(_cache(spr, q_block=64, **chunk)) >= 32 * 8 * 1024 * 4
+    chunk.update(T=32768, max_chunk=32768, max_pages=8192)
+    assert spr.sparsepr_paged_workspace_bytes(_cache(spr, q_block=1, **chunk)) < 1 << 28
 
 
 @pytest.mark.parametrize("kw", [dict(), dict(n_select=4, q_block=40), dict(Hq=4096, Hkv=1, n_select=4, q_block=40)])
