@@ -282,12 +282,14 @@ sparsepr_status sparsepr_rope_frequencies(const sparsepr_rope_params* p, double*
     const int dim = p->axis_dim[ax];
     double base = p->theta;
     if (p->scaling == 2 && dim > 2) base *= pow(p->factor, dim / (dim - 2.0));
-    // scaling 3: the pairs that turn beta_fast and beta_slow times within orig_len
+    // scaling 3: the pairs that turn beta_fast and beta_slow times within orig_len.  The ramp may end
+    // behind the last pair (dim / 2 - 1), which then keeps a share of its frequency: with theta 10,000
+    // the slowest pair still turns once within 54,000 positions or more.
     double lo = 0.0, hi = 0.0;
     if (p->scaling == 3) {
       auto pair_of = [&](double turns) { return dim * log(p->orig_len / (turns * two_pi)) / (2.0 * log(p->theta)); };
       lo = fmax(floor(pair_of(p->beta_fast)), 0.0);
-      hi = fmin(ceil(pair_of(p->beta_slow)), dim / 2 - 1.0);
+      hi = fmin(ceil(pair_of(p->beta_slow)), dim - 1.0);
     }
     for (int j = 0; j < dim / 2; ++j) {
       double w = pow(base, -2.0 * j / dim);

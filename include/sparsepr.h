@@ -353,7 +353,11 @@ typedef struct {
                               2 base: theta replaced by theta factor^(axis_dim/(axis_dim - 2));
                               3 by parts: pairs that turn beta_fast times or more within orig_len
                               positions keep their frequency, those that turn beta_slow times or
-                              less have it divided by factor, a linear ramp over j in between      */
+                              less have it divided by factor, and those in between mix the two: with
+                              c(t) = axis_dim ln(orig_len/(2 pi t)) / (2 ln theta) the pair that turns
+                              t times, lo = max(floor c(beta_fast), 0), hi = min(ceil c(beta_slow),
+                              axis_dim - 1), the frequency times 1 - r + r/factor with
+                              r = (j - lo) / max(hi - lo, 0.001) limited to [0, 1]                 */
   int orig_len;            /* scaling 3: positions the frequencies were made for (>= 1)             */
   double theta;            /* > 0 (10000)                                                           */
   double factor;           /* > 0 (1)                                                               */

@@ -100,6 +100,25 @@ def test_parts_with_a_long_axis_keeps_and_divides(spr):
     assert torch.all(parts <= plain) and torch.all(parts >= plain / 8 * (1 - 1e-12))
 
 
+@pytest.mark.parametrize("dim,orig,factor,lo,hi", [
+    # the pair that turns t times is dim ln(orig / (2 pi t)) / (2 ln 10000): 40.2 and 64.3, 45.0 and 69.1,
+    # 13.8 and 22.1, and 26.7 and 50.7 of the pairs 0 .. 63 (0 .. 21)
+    (128, 65536, 4.0, 40, 65), (128, 131072, 4.0, 45, 70), (44, 65536, 8.0, 13, 23), (128, 9216, 4.0, 26, 51),
+])
+def test_parts_ramp_may_end_behind_the_last_pair(spr, dim, orig, factor, lo, hi):
+    """A long original length: the slowest pair turns more than beta_slow times, so none has its
+    frequency divided by the whole factor."""
+    kw = dict(rot_dim=dim, axis_dim=[dim])
+    got = spr.sparsepr_rope_frequencies(spr.RopeParams.make(1, 1, 1, 128, scaling="parts", factor=factor, orig_len=orig, **kw))
+    plain = spr.sparsepr_rope_frequencies(spr.RopeParams.make(1, 1, 1, 128, **kw))
+    for j in range(dim // 2):
+        share = min(max((j - lo) / (hi - lo), 0.0), 1.0)
+        want = 1.0 - share + share / factor
+        assert abs(got[j] / plain[j] - want) <= 16 * 2.0 ** -53, j      # a few roundings of 2^-53
+        turns = orig / (2 * math.pi) * 10000.0 ** (-2.0 * j / dim)
+        assert turns < 32 or share == 0.0
+        assert (turns <= 1) == (share == 1.0)
+
 def _cache(spr, **kw):
     base = dict(B=3, Hq=8, Hkv=2, d=64, page=32, n_pages=50, max_pages=10, T=40, max_chunk=20)
     st = {k: kw.pop(k) for k in list(kw) if k.endswith("_stride")}
