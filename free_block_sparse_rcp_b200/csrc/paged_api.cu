@@ -102,7 +102,7 @@ sparsepr_status check_rope(const sparsepr_rope_params* p) {
 
 double rope_magnitude(const sparsepr_rope_params& p) {
   if (p.magnitude > 0.0) return p.magnitude;
-  return p.scaling == 3 ? 0.1 * log(p.factor) + 1.0 : 1.0;
+  return p.scaling == 3 && p.factor > 1.0 ? 0.1 * log(p.factor) + 1.0 : 1.0;
 }
 
 void rope_strides(const sparsepr_rope_params& p, int heads, const long long* s, long long* out) {

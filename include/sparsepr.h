@@ -362,7 +362,7 @@ typedef struct {
   double theta;            /* > 0 (10000)                                                           */
   double factor;           /* > 0 (1)                                                               */
   double beta_fast, beta_slow; /* scaling 3: beta_fast > beta_slow > 0 (32 and 1)                   */
-  double magnitude;        /* m; 0 means 1, or 0.1 ln(factor) + 1 with scaling 3                    */
+  double magnitude;        /* m; 0 means 1, or 0.1 ln(factor) + 1 with scaling 3 and factor > 1     */
   long long x_stride[3], y_stride[3];    /* element strides of batch, head and token of the first
                               tensor's input and output; all three 0 means contiguous [B,H,N,d].
                               The last dimension is contiguous; an output stride may not be 0.     */

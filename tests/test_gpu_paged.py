@@ -168,6 +168,17 @@ def test_rope_gradient(spr, gpu):
         assert abs(diff - g[0, 1, 3, i].item()) <= scale
 
 
+@pytest.mark.parametrize("factor,want", [(8.0, 1.0 + 0.1 * math.log(8.0)), (1.0, 1.0), (0.5, 1.0), (1e-6, 1.0)])
+def test_rope_default_magnitude_by_parts(spr, gpu, factor, want):
+    """At position 0 a row is only multiplied: by 0.1 ln(factor) + 1, and by 1 for factors up to 1."""
+    x = torch.ones(1, 1, 2, 64, device=gpu)
+    p = spr.RopeParams.make(1, 1, 2, 64, dtype=F32, scaling="parts", factor=factor, orig_len=4096)
+    y = torch.empty_like(x)
+    spr.sparsepr_rope(p, x, torch.zeros(1, 2, dtype=torch.int32, device=gpu), spr.rope_frequencies(p, gpu), y)
+    # the magnitude's rounding to 32 bits; the sine is 0 and the cosine 1
+    assert torch.all((y.double() - want).abs() <= E24 * want)
+
+
 # ---------------------------------------------------------------------------
 # The cache
 # ---------------------------------------------------------------------------
