@@ -75,10 +75,19 @@ struct Vec {
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
   }
+  // the first n pairs from v, the others as they are in w (bits: an infinity in one of them must not
+  // meet the 0 sine of its partner)
+  static __device__ __forceinline__ uint4 pack_pairs(const float* v, const uint4& w, int n) {
+    const uint4 p = pack(v);
+    if constexpr (sizeof(T) == 4)
+      return make_uint4(p.x, p.y, n > 1 ? p.z : w.z, n > 1 ? p.w : w.w);       // n >= 1
+    else
+      return make_uint4(p.x, n > 1 ? p.y : w.y, n > 2 ? p.z : w.z, n > 3 ? p.w : w.w);
+  }
 };
 
 // How a row is divided among threads.
-//   kInter: one 16-byte chunk, holding whole pairs (pairs past rot/2 turn by 0)
+//   kInter: one 16-byte chunk, holding whole pairs (those past rot/2 are copied)
 //   kHalf:  chunk c of the first half with chunk c of the second, then the copied chunks
 //   kPair:  one pair, one copied element or (wide) one 16-byte chunk past the rotated part, for
 //           rotations that 16-byte chunks do not fit: 2 x 16 heads of 4,000 bf16 rows of d 128, of
@@ -150,7 +159,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
         const float2 cs = turn<sizeof(T) == 4>((double)pos[ax.of(p) * stride] * a.freq[p]);
         c[i] = cs.x * a.mag;
         s[i] = cs.y * (a.mag * a.sign);
-      } else {   // kInter: copied pairs of a chunk that the rotation ends in
+      } else {   // kInter: pairs that pack_pairs copies
         c[i] = 1.f;
         s[i] = 0.f;
       }
@@ -177,7 +186,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
             va[2 * i] = p * c[i] - q * s[i];
             va[2 * i + 1] = p * s[i] + q * c[i];
           }
-          out = Vec<T>::pack(va);
+          out = Vec<T>::pack_pairs(va, wa, half - p0);
         }
         *reinterpret_cast<uint4*>(y + h * yh + e0) = out;
       } else if (MODE == kHalf) {
@@ -447,7 +456,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
             }
             *reinterpret_cast<uint4*>(kp + h * hstep + e1) = Vec<T>::pack(vb);
           }
-          cur.ka[i] = Vec<T>::pack(va);
+          cur.ka[i] = MODE == kInter ? Vec<T>::pack_pairs(va, cur.ka[i], half - p0) : Vec<T>::pack(va);
         }
         *reinterpret_cast<uint4*>(kp + h * hstep + e0) = cur.ka[i];
       }

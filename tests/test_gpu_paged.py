@@ -179,6 +179,41 @@ def test_rope_default_magnitude_by_parts(spr, gpu, factor, want):
     assert torch.all((y.double() - want).abs() <= E24 * want)
 
 
+# bit patterns that arithmetic would change: infinities, -0, quiet and signalling NaNs with payloads
+ODD_BITS = {BF: (torch.int16, [0x7f80, -0x80, -0x8000, 0x7fc5, 0x7f85, -0x3a, 0x0001]),
+            FP: (torch.int16, [0x7c00, -0x400, -0x8000, 0x7e05, 0x7c05, -0x1a, 0x0001]),
+            F32: (torch.int32, [0x7f800000, -0x800000, -0x80000000, 0x7fc00005, 0x7f800005, -0x3ffffa, 0x00000001])}
+
+
+def odd_tail(x, rot, seed):
+    """x with such patterns in some of the elements from rot on."""
+    it, bits = ODD_BITS[x.dtype]
+    y = x.clone().view(it)
+    pick = torch.randint(0, 2 * len(bits), y[..., rot:].shape, generator=gen(seed))
+    vals = torch.tensor(bits, dtype=it)[pick % len(bits)]
+    y[..., rot:] = torch.where(pick < len(bits), vals, y[..., rot:])
+    return y.view(x.dtype), it
+
+
+@pytest.mark.parametrize("dt", [BF, FP, F32])
+@pytest.mark.parametrize("layout,d,rot", [("interleaved", 64, 22), ("interleaved", 64, 2), ("interleaved", 128, 126), ("half", 64, 22),
+                                          ("half", 64, 32), ("interleaved", 6, 4)])
+def test_rope_copies_what_is_behind_the_rotation(spr, gpu, layout, d, rot, dt):
+    """Elements rot_dim .. d - 1 keep their bits, and what they hold does not reach the others."""
+    H, N = 3, 37
+    x = torch.randn(1, H, N, d, generator=gen(81)).to(dt)
+    odd, it = odd_tail(x, rot, 82)
+    p = spr.RopeParams.make(1, H, N, d, dtype=dt, rot_dim=rot, layout=layout)
+    pos = torch.arange(5, 5 + N, dtype=torch.int32, device=gpu)[None]
+    f = spr.rope_frequencies(p, gpu)
+    for call in (spr.sparsepr_rope, spr.sparsepr_rope_backward):
+        plain, got = torch.empty_like(x, device=gpu), torch.empty_like(x, device=gpu)
+        call(p, x.to(gpu), pos, f, plain)
+        call(p, odd.to(gpu), pos, f, got)
+        assert torch.equal(got.view(it)[..., rot:].cpu(), odd.view(it)[..., rot:])
+        assert torch.equal(got[..., :rot], plain[..., :rot])
+
+
 # ---------------------------------------------------------------------------
 # The cache
 # ---------------------------------------------------------------------------
@@ -582,6 +617,25 @@ def test_append_bad_page(spr, gpu):
     pid = int(s.table[0, 2])
     assert torch.equal(torch.nan_to_num(s.dev["kp"][pid]), torch.nan_to_num(before[pid]))
     assert torch.all(s.dev["kp"][int(s.table[1, 1]), 0, 9:14] == 1)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("layout,rot", [("interleaved", 22), ("interleaved", 126), ("half", 22), ("half", 32)])
+def test_append_copies_what_is_behind_the_rotation(spr, gpu, layout, rot, dt):
+    """Elements rot_dim .. d - 1 of the keys, and the values, keep their bits."""
+    d, n = 128, 37
+    s = Scene(spr, gpu, [n], [n + 20], Hq=3, Hkv=3, d=d, page=16, dt=dt, seed=83)
+    K, it = odd_tail(torch.randn(n, 3, d, generator=gen(84)).to(dt), rot, 85)
+    V, _ = odd_tail(torch.randn(n, 3, d, generator=gen(86)).to(dt), 0, 87)
+    rp = spr.RopeParams.make(1, 3, n, d, dtype=dt, rot_dim=rot, layout=layout)
+    pos = torch.arange(20, 20 + n, dtype=torch.int32, device=gpu)[None]
+    spr.sparsepr_cache_append(s.p, K.to(gpu), V.to(gpu), *s.seqs(), s.dev["kp"], s.dev["vp"], s.dev["km"], s.ws, rope=rp, pos=pos,
+                              freq=spr.rope_frequencies(rp, gpu))
+    slot = torch.arange(20, 20 + n)
+    pid = s.table[0][slot // 16].long()
+    kp, vp = s.dev["kp"].cpu().view(it), s.dev["vp"].cpu().view(it)
+    assert torch.equal(kp[pid, :, slot % 16][..., rot:], K.view(it)[..., rot:])
+    assert torch.equal(vp[pid, :, slot % 16], V.view(it))
 
 
 # ---------------------------------------------------------------------------
