@@ -448,14 +448,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_page_score(SelectArgs a) {
   float eps = tiny ? INFINITY : 0.f;
   int id[UN];
 #pragma unroll
-  for (int s = 0; s < UN; ++s) id[s] = p0 + s * PPB + (tid >> 3) < p1 ? table[p0 + s * PPB + (tid >> 3)] : -2;
+  for (int s = 0; s < UN; ++s) id[s] = p0 + s * PPB + (tid >> 3) < p1 ? table[p0 + s * PPB + (tid >> 3)] : -1;
   for (int j0 = p0; j0 < p1; j0 += PPB * UN) {
     uint4 w[UN][CPL / 8];
     bool ok[UN];
 #pragma unroll
     for (int s = 0; s < UN; ++s) {
       ok[s] = id[s] >= 0 && id[s] < a.p.n_pages;
-      if (!ok[s] && id[s] != -2 && sub == 0) set_error(a.p.err, DERR_INDEX);
+      if (!ok[s] && j0 + s * PPB + (tid >> 3) < p1 && sub == 0) set_error(a.p.err, DERR_INDEX);
       const T* row = (const T*)a.km + ((size_t)(ok[s] ? id[s] : 0) * a.p.Hkv + h) * D;
 #pragma unroll
       for (int c = 0; c < CPL / 8; ++c) w[s][c] = *reinterpret_cast<const uint4*>(row + c * 64 + sub * 8);
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_page_score(SelectArgs a) {
 #pragma unroll
     for (int s = 0; s < UN; ++s) {
       const int j = j0 + (UN + s) * PPB + (tid >> 3);
-      id[s] = j < p1 ? table[j] : -2;
+      id[s] = j < p1 ? table[j] : -1;
     }
 #pragma unroll
     for (int s = 0; s < UN; ++s) {
@@ -602,14 +602,14 @@ __global__ void __launch_bounds__(kGroupThreads, 2) k_group_score(SelectArgs a) 
     float kk = 0.f;                  // largest sum of squares of this lane's columns of a page
     int id[UN];
 #pragma unroll
-    for (int s = 0; s < UN; ++s) id[s] = p0 + s * PPB + (tid >> 3) < p1 ? table[p0 + s * PPB + (tid >> 3)] : -2;
+    for (int s = 0; s < UN; ++s) id[s] = p0 + s * PPB + (tid >> 3) < p1 ? table[p0 + s * PPB + (tid >> 3)] : -1;
     for (int j0 = p0; j0 < p1; j0 += PPB * UN) {
       uint4 w[UN][CPL / 8];
       bool ok[UN];
 #pragma unroll
       for (int s = 0; s < UN; ++s) {
         ok[s] = id[s] >= 0 && id[s] < a.p.n_pages;
-        if (!ok[s] && id[s] != -2 && sub == 0) set_error(a.p.err, DERR_INDEX);
+        if (!ok[s] && j0 + s * PPB + (tid >> 3) < p1 && sub == 0) set_error(a.p.err, DERR_INDEX);
         const T* row = (const T*)a.km + ((size_t)(ok[s] ? id[s] : 0) * a.p.Hkv + h) * D;
 #pragma unroll
         for (int c = 0; c < CPL / 8; ++c) w[s][c] = *reinterpret_cast<const uint4*>(row + c * 64 + sub * 8);
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kGroupThreads, 2) k_group_score(SelectArgs a) 
 #pragma unroll
       for (int s = 0; s < UN; ++s) {
         const int j = j0 + (UN + s) * PPB + (tid >> 3);
-        id[s] = j < p1 ? table[j] : -2;
+        id[s] = j < p1 ? table[j] : -1;
       }
       uint64_t x2[UN][U], k2[UN];
 #pragma unroll

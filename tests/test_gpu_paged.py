@@ -781,6 +781,24 @@ def test_bad_lists_are_errors(spr, gpu):
             assert torch.isnan(O[new[0]:sum(new)]).all(), what
 
 
+@pytest.mark.parametrize("units", [1, 42])       # 42: scored four at a time
+@pytest.mark.parametrize("pid", [-2, -1, -2 ** 31, -3, "n_pages"])
+def test_select_bad_page_ids_are_errors(spr, gpu, pid, units):
+    """Any id out of [0, n_pages) in a visible entry is error 1 and scores lowest."""
+    s = Scene(spr, gpu, [units], [16 * 90], Hq=2, Hkv=2, d=64, page=16, dt=BF, q_block=1, n_select=87, seed=93)
+    t, km = s.table.clone(), s.km.clone()
+    sel, cnt = s.select()
+    assert spr.sparsepr_paged_error(s.ws) == 0
+    km[int(t[0, 33])] = float("nan")             # the lowest score of the definition
+    t[0, 33] = s.n_pages if pid == "n_pages" else pid
+    s.dev["table"] = t.to(gpu)
+    sel, cnt = s.select()
+    assert spr.sparsepr_paged_error(s.ws) == 1
+    want, wc = R.select(s.Q, s.new, s.kv, s.table, km, 16, 1, 1, 87, 0, 0)
+    assert torch.equal(cnt.cpu(), wc) and torch.equal(sel.cpu(), want)
+    assert not torch.any(sel[-1] == 33)
+
+
 @pytest.mark.parametrize("Hq", [2, 40])
 def test_limits_beyond_the_rows_of_the_call(spr, gpu, Hq):
     """A max_chunk and a q_block that no sequence can reach count as T."""
