@@ -87,22 +87,25 @@ struct Vec {
 };
 
 // How a row is divided among threads.
-//   kInter: one 16-byte chunk, holding whole pairs (those past rot/2 are copied)
+//   kInter: one 16-byte chunk, holding whole pairs
+//   kMixed: kInter with a rotation that ends inside a chunk, whose other pairs are copied (the loaded words
+//           have to be kept for them: 1.3 us of 213 us on 32,760 tokens x 80 heads that need it nowhere)
 //   kHalf:  chunk c of the first half with chunk c of the second, then the copied chunks
 //   kPair:  one pair, one copied element or (wide) one 16-byte chunk past the rotated part, for
 //           rotations that 16-byte chunks do not fit: 2 x 16 heads of 4,000 bf16 rows of d 128, of
 //           which 22 elements turn, take 20 us, 39 us with the copied elements one by one
-enum RopeMode { kInter = 0, kHalf = 1, kPair = 2 };
+enum RopeMode { kInter = 0, kHalf = 1, kPair = 2, kMixed = 3 };
+constexpr bool inter(int mode) { return mode == kInter || mode == kMixed; }
 
 template <typename T, int MODE>
 struct RowUnits {
   static constexpr int E = Vec<T>::E;
   // pairs a unit turns, at most
-  static constexpr int P = MODE == kInter ? E / 2 : (MODE == kHalf ? E : 1);
+  static constexpr int P = inter(MODE) ? E / 2 : (MODE == kHalf ? E : 1);
   // kPair: first element of the copied chunks
   static __host__ __device__ int tail(int d, int rot, bool wide) { return wide ? (rot + E - 1) / E * E : d; }
   static __host__ __device__ int count(int d, int rot, bool wide = false) {
-    if (MODE == kInter) return d / E;
+    if (inter(MODE)) return d / E;
     if (MODE == kHalf) return rot / 2 / E + (d - rot) / E;
     const int t = tail(d, rot, wide);
     return rot / 2 + (t - rot) + (d - t) / E;
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
   // first element, partner element (kHalf, kPair) and whether the unit turns
   int e0, e1 = 0, p0;
   bool turns, wide = false;       // wide: a chunk of kPair
-  if (MODE == kInter) {
+  if (inter(MODE)) {
     e0 = u * E;
     p0 = e0 / 2;
     turns = p0 < half;
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
         const float2 cs = turn<sizeof(T) == 4>((double)pos[ax.of(p) * stride] * a.freq[p]);
         c[i] = cs.x * a.mag;
         s[i] = cs.y * (a.mag * a.sign);
-      } else {   // kInter: pairs that pack_pairs copies
+      } else {   // kMixed: pairs that pack_pairs copies
         c[i] = 1.f;
         s[i] = 0.f;
       }
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
                                              : (int)(((long long)blockIdx.y - a.H[0] % gy + gy) % gy);
     auto one = [&](int h, const uint4& wa, const uint4& wb) {
       float va[E], vb[E];
-      if (MODE == kInter) {
+      if (inter(MODE)) {
         uint4 out = wa;
         if (turns) {
           Vec<T>::unpack(wa, va);
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, long long uni
             va[2 * i] = p * c[i] - q * s[i];
             va[2 * i + 1] = p * s[i] + q * c[i];
           }
-          out = Vec<T>::pack_pairs(va, wa, half - p0);
+          out = MODE == kMixed ? Vec<T>::pack_pairs(va, wa, half - p0) : Vec<T>::pack(va);
         }
         *reinterpret_cast<uint4*>(y + h * yh + e0) = out;
       } else if (MODE == kHalf) {
@@ -280,7 +283,7 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_rope_m(const RopeArgs& a, cudaStream_t st) {
   constexpr int E = Vec<T>::E;
-  if (a.vec && a.layout == 1) return launch_rope_t<T, kInter>(a, st);
+  if (a.vec && a.layout == 1) return a.rot % E ? launch_rope_t<T, kMixed>(a, st) : launch_rope_t<T, kInter>(a, st);
   if (a.vec && (a.rot / 2) % E == 0) return launch_rope_t<T, kHalf>(a, st);
   return launch_rope_t<T, kPair>(a, st);
 }
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
   const int u = (int)(gid - (long long)row * upr);
   int e0, e1 = 0, p0;
   bool turns = false, wide = false;
-  if (MODE == kInter) {
+  if (inter(MODE)) {
     e0 = u * E;
     p0 = e0 / 2;
     turns = ROPE && p0 < half;
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
         if (ROPE && turns) {
           float va[E], vb[E];
           Vec<T>::unpack(cur.ka[i], va);
-          if (MODE == kInter) {
+          if (inter(MODE)) {
 #pragma unroll
             for (int k = 0; k < P; ++k) {
               const float p = va[2 * k], q = va[2 * k + 1];
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
             }
             *reinterpret_cast<uint4*>(kp + h * hstep + e1) = Vec<T>::pack(vb);
           }
-          cur.ka[i] = MODE == kInter ? Vec<T>::pack_pairs(va, cur.ka[i], half - p0) : Vec<T>::pack(va);
+          cur.ka[i] = MODE == kMixed ? Vec<T>::pack_pairs(va, cur.ka[i], half - p0) : Vec<T>::pack(va);
         }
         *reinterpret_cast<uint4*>(kp + h * hstep + e0) = cur.ka[i];
       }
@@ -602,7 +605,7 @@ cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_append_m(const AppendArgs& a, cudaStream_t st) {
   if (!a.pos) return launch_append_t<T, kInter, false>(a, st);
-  if (a.layout == 1) return launch_append_t<T, kInter, true>(a, st);
+  if (a.layout == 1) return a.rot % Vec<T>::E ? launch_append_t<T, kMixed, true>(a, st) : launch_append_t<T, kInter, true>(a, st);
   if ((a.rot / 2) % Vec<T>::E == 0) return launch_append_t<T, kHalf, true>(a, st);
   return launch_append_t<T, kPair, true>(a, st);
 }
