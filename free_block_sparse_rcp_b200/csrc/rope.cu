@@ -317,6 +317,14 @@ __device__ __forceinline__ int find_seq(const int* __restrict__ q_start, int B, 
   return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
 }
 
+// Whether the sequence with these entries is appended: its rows lie within the call's, its new tokens
+// within max_chunk, its length within the table.  Otherwise nothing of it is written: rows moved to the
+// slots of a length cut to the table would replace the last keys of a full cache, and the page means
+// count on the pages that a chunk of max_chunk can touch.
+__device__ __forceinline__ bool usable(const AppendArgs& a, int lo, int hi, int len) {
+  return lo >= 0 && hi >= lo && hi <= a.T && hi - lo <= a.max_chunk && len >= 0 && len <= a.max_pages * a.page;
+}
+
 template <typename T, int MODE, bool ROPE>
 __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
   using U = RowUnits<T, MODE>;
@@ -390,10 +398,11 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
     }
   }
   if (!live || b < 0 || b >= a.B || row < a.q_start[b]) return;
-  const int qs = a.q_start[b], qe = a.q_start[b + 1], lenr = a.kv_len[b];
-  const int n = qe - qs, len = min(max(lenr, 0), a.max_pages * page);
-  if (u == 0 && row == max(qs, 0) && blockIdx.y == 0 && (qs < 0 || qe > a.T || len != lenr || n > a.max_chunk))
-    set_error(a.err, DERR_INDEX);
+  const int qs = a.q_start[b], qe = a.q_start[b + 1], len = a.kv_len[b], n = qe - qs;
+  if (!usable(a, qs, qe, len)) {
+    if (u == 0 && row == max(qs, 0) && blockIdx.y == 0) set_error(a.err, DERR_INDEX);
+    return;
+  }
   const int slot = len - n + (row - qs);
   if (slot < 0 || slot >= len) return;
   const int j = slot / page;
@@ -482,10 +491,8 @@ __global__ void __launch_bounds__(kMeanThreads) k_page_means(AppendArgs a, int t
   const int tid = threadIdx.x, page = a.page;
   // sequence b and its touched page: pages floor((len - n) / page) .. floor((len - 1) / page)
   auto pages_of = [&](int b) -> int {
-    const int lo = min(max(a.q_start[b], 0), a.T);
-    const int n = max(0, min(a.q_start[b + 1], a.T) - lo);
-    const int len = min(max(a.kv_len[b], 0), a.max_pages * page);
-    if (n == 0 || len == 0) return 0;
+    const int lo = a.q_start[b], hi = a.q_start[b + 1], len = a.kv_len[b], n = hi - lo;
+    if (n <= 0 || len == 0 || !usable(a, lo, hi, len)) return 0;
     return (len - 1) / page - max(len - n, 0) / page + 1;
   };
   int b, jt;
@@ -532,10 +539,9 @@ __global__ void __launch_bounds__(kMeanThreads) k_page_means(AppendArgs a, int t
       return;
     }
   }
-  const int q0 = min(max(a.q_start[b], 0), a.T), n = max(0, min(a.q_start[b + 1], a.T) - q0);
-  const int len = min(max(a.kv_len[b], 0), a.max_pages * page);
+  const int q0 = a.q_start[b], q1 = a.q_start[b + 1], n = q1 - q0, len = a.kv_len[b];
   const int j = max(len - n, 0) / page + jt, base = j * page, h = blockIdx.y;
-  const bool used = n > 0 && base < len;
+  const bool used = n > 0 && usable(a, q0, q1, len) && base < len;
   const int pid = used ? a.table[(size_t)b * a.max_pages + j] : -1;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the rows are in their slots
   if (pid < 0 || pid >= a.n_pages) return;        // recorded by k_cache_rows

@@ -434,7 +434,9 @@ SPARSEPR_API size_t sparsepr_paged_workspace_bytes(const sparsepr_cache_params* 
  * rotated on the way: rope's rot_dim, layout, axes and magnitude count, pos is int32
  * [n_axes, T] and rope_freq double [rot_dim/2] (both device); its other fields are not read
  * except that d must agree.  Pages being written must belong to one sequence of the call.
- * A page id out of [0, n_pages) is device error 1 and its rows are not written.         */
+ * A page id out of [0, n_pages) is device error 1 and its rows are not written; a kv_len out
+ * of [0, max_pages * page], more than max_chunk new tokens or rows out of [0, T) are device
+ * error 1 and nothing of that sequence is written.                                      */
 SPARSEPR_API sparsepr_status sparsepr_cache_append(const sparsepr_cache_params* p, const void* K, const void* V,
                                                    const int* q_start, const int* kv_len, const int* page_table,
                                                    void* k_pages, void* v_pages, void* k_mean,

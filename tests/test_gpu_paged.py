@@ -638,6 +638,43 @@ def test_append_copies_what_is_behind_the_rotation(spr, gpu, layout, rot, dt):
     assert torch.equal(vp[pid, :, slot % 16], V.view(it))
 
 
+@pytest.mark.parametrize("what", ["full", "long", "negative", "chunk", "rows", "before"])
+def test_append_of_a_sequence_with_bad_inputs_writes_nothing(spr, gpu, what):
+    """A cache length beyond the table, more new tokens than max_chunk, offsets out of the rows: error 1,
+    the sequence's pages and means stay as they were, the other sequence's rows arrive."""
+    s = Scene(spr, gpu, [40, 21], [64, 100], Hq=2, Hkv=2, d=64, page=16, dt=BF, seed=88, max_pages=7, max_chunk=50)
+    bad = 1 if what == "rows" else 0
+    t = s.table.clone()
+    t[0, 4:] = t[0, 0]                            # entries that a wrong length reaches: a page of the same sequence
+    qs, ln = s.q_start.clone(), s.kv_len.clone()
+    if what == "full":
+        ln[bad] = 7 * 16 + 1
+    if what == "long":
+        ln[bad] = 2 ** 31 - 1
+    if what == "negative":
+        ln[bad] = -1
+    if what == "chunk":
+        s.p.max_chunk = 21
+    if what == "rows":                            # the last sequence promises rows behind the call's
+        qs[2] += 3
+    if what == "before":                          # the first one rows before them
+        qs[0] = -2
+    before = {k: s.dev[k].cpu().view(torch.int16).clone() for k in ("kp", "vp", "km")}
+    K = torch.randn(61, 2, 64, generator=gen(89)).to(BF)
+    V = torch.randn(61, 2, 64, generator=gen(90)).to(BF)
+    spr.sparsepr_cache_append(s.p, K.to(gpu), V.to(gpu), qs.to(gpu), ln.to(gpu), t.to(gpu), s.dev["kp"], s.dev["vp"], s.dev["km"], s.ws)
+    assert spr.sparsepr_paged_error(s.ws) == 1
+    mine = s.table[bad][:4 if bad == 0 else 7].long()
+    for k, v in before.items():
+        assert torch.equal(s.dev[k].cpu().view(torch.int16)[mine], v[mine]), k
+    other = 1 - bad
+    at, n, length = (40, 21, 100) if other else (0, 40, 64)
+    slot = torch.arange(length - n, length)
+    pid = s.table[other][slot // 16].long()
+    assert torch.equal(s.dev["kp"].cpu()[pid, :, slot % 16], K[at:at + n])
+    assert torch.equal(s.dev["vp"].cpu()[pid, :, slot % 16], V[at:at + n])
+
+
 # ---------------------------------------------------------------------------
 # Selection, and attention over the lists
 # ---------------------------------------------------------------------------
