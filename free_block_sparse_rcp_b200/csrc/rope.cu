@@ -480,6 +480,9 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
 }
 
 constexpr int kMeanThreads = 128;
+// The sums are kept 2^-7 of their size (exactly; a page has at most 128 rows), so that bf16 keys near
+// fp32's largest value have a mean.
+constexpr float kMeanScale = 1.f / 128.f;
 
 // grid (page slots that the call can touch, Hkv): tp slots per sequence, or (tp = 0) slots counted
 // sequence by sequence.
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(kMeanThreads) k_page_means(AppendArgs a, int t
       float v[E];
       Vec<T>::unpack(w[i], v);
 #pragma unroll
-      for (int k = 0; k < E; ++k) acc[k] += v[k];
+      for (int k = 0; k < E; ++k) acc[k] = fmaf(v[k], kMeanScale, acc[k]);
     }
   }
 #pragma unroll
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(kMeanThreads) k_page_means(AppendArgs a, int t
     float s = 0.f;
 #pragma unroll
     for (int g = 0; g < RG; ++g) s += red[g][tid];
-    ((T*)a.km)[((size_t)pid * a.Hkv + h) * D + tid] = from_f32<T>(s / (float)rows);
+    ((T*)a.km)[((size_t)pid * a.Hkv + h) * D + tid] = from_f32<T>(s / (float)rows * (1.f / kMeanScale));
   }
 }
 

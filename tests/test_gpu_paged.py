@@ -675,6 +675,21 @@ def test_append_of_a_sequence_with_bad_inputs_writes_nothing(spr, gpu, what):
     assert torch.equal(s.dev["vp"].cpu()[pid, :, slot % 16], V[at:at + n])
 
 
+@pytest.mark.parametrize("dt,big", [(BF, 3e38), (FP, 5.9e4)])
+def test_means_of_large_keys(spr, gpu, dt, big):
+    """Keys near the end of the type's range: their sum leaves 32 bits, their mean does not."""
+    n, d, page = 150, 64, 128
+    s = Scene(spr, gpu, [n], [n], Hq=1, Hkv=1, d=d, page=page, dt=dt, seed=91)
+    K = (big * (1 + 0.1 * torch.rand(n, 1, d, generator=gen(92)) * torch.where(torch.arange(d) % 3 == 0, -1.0, 1.0))).to(dt)
+    K[:, :, 1::4] = -K[:, :, 1::4]
+    spr.sparsepr_cache_append(s.p, K.to(gpu), K.to(gpu), *s.seqs(), s.dev["kp"], s.dev["vp"], s.dev["km"], s.ws)
+    for j, r in ((0, 128), (1, 22)):
+        pid = int(s.table[0, j])
+        k = s.dev["kp"][pid, :, :r].cpu().double()
+        mean = k.mean(1)
+        assert torch.all((s.dev["km"][pid].cpu().double() - mean).abs() <= R.HALF_STEP[dt] * mean.abs() + 128 * E24 * k.abs().mean(1))
+
+
 # ---------------------------------------------------------------------------
 # Selection, and attention over the lists
 # ---------------------------------------------------------------------------
