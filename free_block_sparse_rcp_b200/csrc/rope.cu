@@ -302,13 +302,18 @@ cudaError_t launch_rope_m(const RopeArgs& a, cudaStream_t st) {
 // two short kernels (angle, load, store; then table, rows, mean).  One token of each of 64
 // sequences takes 6.8 us.
 
-// Sequence that holds packed row t (-1: none), by the whole warp: 32 probes a step.
-__device__ __forceinline__ int find_seq(const int* __restrict__ q_start, int B, int t, int lane) {
+// Sequence that holds packed row t (-1: none), by the whole warp: 32 probes a step.  v: this lane's
+// first probe, first_probe().
+__device__ __forceinline__ int first_probe(const int* __restrict__ q_start, int B, int lane) {
+  const int i = lane * ((B + 31) >> 5);
+  return i < B ? q_start[i] : 0;
+}
+__device__ __forceinline__ int find_seq(const int* __restrict__ q_start, int B, int t, int lane, int v) {
   int lo = 0, n = B;            // the last b in [lo, lo + n) with q_start[b] <= t
   while (n > 1) {
     const int step = (n + 31) >> 5;
     const int i = lane * step;
-    const bool le = i < n && q_start[lo + i] <= t;
+    const bool le = i < n && (n == B ? v : q_start[lo + i]) <= t;
     const int cnt = __popc(__ballot_sync(0xffffffffu, le));
     const int at = cnt > 0 ? (cnt - 1) * step : 0;
     lo += at;
@@ -317,12 +322,13 @@ __device__ __forceinline__ int find_seq(const int* __restrict__ q_start, int B, 
   return q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
 }
 
-// Whether the sequence with these entries is appended: its rows lie within the call's, its new tokens
-// within max_chunk, its length within the table.  Otherwise nothing of it is written: rows moved to the
+// Whether the sequence with these entries is appended: its rows lie within the call's and between the
+// first and the last offset, its new tokens within max_chunk, its length within the table.  Otherwise nothing of it is written: rows moved to the
 // slots of a length cut to the table would replace the last keys of a full cache, and the page means
 // count on the pages that a chunk of max_chunk can touch.
-__device__ __forceinline__ bool usable(const AppendArgs& a, int lo, int hi, int len) {
-  return lo >= 0 && hi >= lo && hi <= a.T && hi - lo <= a.max_chunk && len >= 0 && len <= a.max_pages * a.page;
+__device__ __forceinline__ bool usable(const AppendArgs& a, int row0, int row1, int lo, int hi, int len) {
+  return lo >= max(row0, 0) && hi >= lo && hi <= min(row1, a.T) && hi - lo <= a.max_chunk && len >= 0 &&
+         len <= a.max_pages * a.page;
 }
 
 template <typename T, int MODE, bool ROPE>
@@ -362,7 +368,10 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
   // its chunks)
   constexpr int VE = Vec<T>::E;
   const int f0 = u * VE < d ? u * VE : -1, f1 = (u + upr) * VE < d ? (u + upr) * VE : -1;
-  const bool live = row < a.T;
+  // rows of no sequence are not read: a call may be padded with rows that its buffers do not hold.  The
+  // offsets that say so come with the search's first probes (loaded before those they cost 0.4 us).
+  const int probe = first_probe(a.q_start, a.B, lane), row1 = a.q_start[a.B], row0 = __shfl_sync(0xffffffffu, probe, 0);
+  const bool live = row < a.T && row >= row0 && row < row1;
   const T* K = (const T*)a.K + (live ? row * a.kst : 0);
   const T* V = (const T*)a.V + (live ? row * a.vst : 0);
   const int gy = gridDim.y;
@@ -387,19 +396,19 @@ __global__ void __launch_bounds__(kRopeThreads) k_cache_rows(AppendArgs a) {
   {
     const int first = __shfl_sync(0xffffffffu, row, 0), last = min(__shfl_sync(0xffffffffu, row, 31), a.T - 1);
     if (first < a.T) {
-      b = find_seq(a.q_start, a.B, first, lane);
+      b = find_seq(a.q_start, a.B, first, lane, probe);
       if (b >= 0 && a.q_start[b + 1] <= last)        // the warp's rows leave the first one's sequence
         while (b < a.B && row >= a.q_start[b + 1]) ++b;
       if (b < 0)                                     // rows that belong to no sequence, or broken offsets
         for (int r = first; r <= last; ++r) {
-          const int f = find_seq(a.q_start, a.B, r, lane);
+          const int f = find_seq(a.q_start, a.B, r, lane, probe);
           if (r == row) b = f;
         }
     }
   }
   if (!live || b < 0 || b >= a.B || row < a.q_start[b]) return;
   const int qs = a.q_start[b], qe = a.q_start[b + 1], len = a.kv_len[b], n = qe - qs;
-  if (!usable(a, qs, qe, len)) {
+  if (!usable(a, row0, row1, qs, qe, len)) {
     if (u == 0 && row == max(qs, 0) && blockIdx.y == 0) set_error(a.err, DERR_INDEX);
     return;
   }
@@ -491,11 +500,11 @@ __global__ void __launch_bounds__(kMeanThreads) k_page_means(AppendArgs a, int t
   constexpr int E = 8, CH = D / E, RG = kMeanThreads / CH, UN = 8;
   __shared__ float red[RG][D];
   __shared__ int sm_find[kMeanThreads / 32 + 2];
-  const int tid = threadIdx.x, page = a.page;
+  const int tid = threadIdx.x, page = a.page, row0 = a.q_start[0], row1 = a.q_start[a.B];
   // sequence b and its touched page: pages floor((len - n) / page) .. floor((len - 1) / page)
   auto pages_of = [&](int b) -> int {
     const int lo = a.q_start[b], hi = a.q_start[b + 1], len = a.kv_len[b], n = hi - lo;
-    if (n <= 0 || len == 0 || !usable(a, lo, hi, len)) return 0;
+    if (n <= 0 || len == 0 || !usable(a, row0, row1, lo, hi, len)) return 0;
     return (len - 1) / page - max(len - n, 0) / page + 1;
   };
   int b, jt;
@@ -544,7 +553,7 @@ __global__ void __launch_bounds__(kMeanThreads) k_page_means(AppendArgs a, int t
   }
   const int q0 = a.q_start[b], q1 = a.q_start[b + 1], n = q1 - q0, len = a.kv_len[b];
   const int j = max(len - n, 0) / page + jt, base = j * page, h = blockIdx.y;
-  const bool used = n > 0 && usable(a, q0, q1, len) && base < len;
+  const bool used = n > 0 && usable(a, row0, row1, q0, q1, len) && base < len;
   const int pid = used ? a.table[(size_t)b * a.max_pages + j] : -1;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the rows are in their slots
   if (pid < 0 || pid >= a.n_pages) return;        // recorded by k_cache_rows

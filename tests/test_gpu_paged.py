@@ -690,6 +690,39 @@ def test_means_of_large_keys(spr, gpu, dt, big):
         assert torch.all((s.dev["km"][pid].cpu().double() - mean).abs() <= R.HALF_STEP[dt] * mean.abs() + 128 * E24 * k.abs().mean(1))
 
 
+def test_append_between_rows_of_no_sequence(spr, gpu):
+    """Rows before the first sequence and behind the last one: the pages are those of the call without
+    them, whatever they hold."""
+    n, front, tail = [40, 1, 0, 9], 37, 300
+    kw = dict(Hq=3, Hkv=3, d=64, page=16, dt=BF, seed=94)
+    s, t = Scene(spr, gpu, n, [64, 100, 5, 30], **kw), Scene(spr, gpu, n, [64, 100, 5, 30], tail_rows=front + tail, **kw)
+    nan = float("nan")
+    K, V = (torch.randn(50, 3, 64, generator=gen(95 + i)).to(BF) for i in range(2))
+    Kp, Vp = (torch.cat([x.new_full((front, 3, 64), nan), x, x.new_full((tail, 3, 64), nan)]) for x in (K, V))
+    for rot in (64, 22):
+        for c, k, v, q0 in ((s, K, V, 0), (t, Kp, Vp, front)):
+            rp = spr.RopeParams.make(1, 3, c.T, 64, rot_dim=rot)
+            pos = torch.full((1, c.T), -1, dtype=torch.int32)
+            pos[0, q0:q0 + 50] = torch.arange(50)
+            spr.sparsepr_cache_append(c.p, k.to(gpu), v.to(gpu), c.dev["q_start"] + q0, c.dev["kv_len"], c.dev["table"], c.dev["kp"],
+                                      c.dev["vp"], c.dev["km"], c.ws, rope=rp, pos=pos.to(gpu), freq=spr.rope_frequencies(rp, gpu))
+            assert spr.sparsepr_paged_error(c.ws) == 0
+        for m in ("kp", "vp", "km"):
+            assert torch.equal(s.dev[m].view(torch.int16), t.dev[m].view(torch.int16)), m
+
+
+def test_append_offsets_out_of_order(spr, gpu):
+    """A sequence that reaches behind the last offset is error 1 and is not written."""
+    s = Scene(spr, gpu, [50, 11], [64, 100], Hq=2, Hkv=2, d=64, page=16, dt=BF, seed=96)
+    before = {k: s.dev[k].cpu().view(torch.int16).clone() for k in ("kp", "vp", "km")}
+    qs = torch.tensor([0, 50, 40], dtype=torch.int32, device=gpu)
+    K = torch.randn(61, 2, 64, generator=gen(97)).to(BF).to(gpu)
+    spr.sparsepr_cache_append(s.p, K, K, qs, s.dev["kv_len"], s.dev["table"], s.dev["kp"], s.dev["vp"], s.dev["km"], s.ws)
+    assert spr.sparsepr_paged_error(s.ws) == 1
+    for k, v in before.items():
+        assert torch.equal(s.dev[k].cpu().view(torch.int16), v), k
+
+
 # ---------------------------------------------------------------------------
 # Selection, and attention over the lists
 # ---------------------------------------------------------------------------
