@@ -41,7 +41,6 @@ constexpr int kSelBins = 2048;
 constexpr int kSelSmemPages = 8192;   // scores and keys in shared memory up to this many pages (96 KB)
 constexpr int kSelExact = 64;         // pages scored again in one step
 constexpr int kSelGroup = 4;          // units that k_group_score scores together
-constexpr long long kSelScores = 1 << 26;   // scores at most that are stored for it (256 MB)
 constexpr double kSelTiny = 7.8886090522101181e-31;   // 2^-100
 
 // largest exponent field of a packed pair's halves, as a bit pattern: >= kInf: not finite
@@ -405,8 +404,8 @@ __device__ void mean_query(const SelectArgs& a, const UnitInfo& u, int h, double
   __syncthreads();
 }
 
-// grid (units x splits, Hkv).  Scores of the split's share of the pages; with one split the
-// block goes on to the list.
+// grid (units x splits, heads) of a batch.  Scores of the split's share of the pages; with one split
+// the block goes on to the list, unless that is too long for shared memory.
 template <typename T, int D>
 __global__ void __launch_bounds__(kSelThreads, 2) k_page_score(SelectArgs a) {
   extern __shared__ __align__(16) unsigned char sm_sel[];
@@ -414,17 +413,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_page_score(SelectArgs a) {
   __shared__ double s_q[D];
   __shared__ float s_eps[kSelThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");     // k_page_pick may get ready
-  const int tid = threadIdx.x, h = blockIdx.y;
-  const int unit = blockIdx.x / a.splits, split = blockIdx.x - unit * a.splits;
+  const int tid = threadIdx.x, h = a.h0 + blockIdx.y;
+  const int nth = blockIdx.x / a.splits, unit = a.u0 + nth, split = blockIdx.x - nth * a.splits;
   UnitInfo u;
   if (!unit_of<kSelThreads>(a, unit, sm_find, u)) return;
   int* hist = reinterpret_cast<int*>(sm_sel);
   // the reduction of the mean query and, later, the keys share the space behind the bins
   unsigned char* rest = sm_sel + kSelBins * 4;
   mean_query<T, D, kSelThreads>(a, u, h, s_q, reinterpret_cast<double(*)[D + 1]>(rest));
-  const size_t list = (size_t)unit * a.p.Hkv + h;
+  const size_t list = (size_t)unit * a.p.Hkv + h, slot = (size_t)nth * a.nh + blockIdx.y;
   const bool stored = a.splits > 1 || a.keys_global;
-  uint32_t* keys = stored ? reinterpret_cast<uint32_t*>(a.scores) + list * a.p.max_pages
+  uint32_t* keys = stored ? reinterpret_cast<uint32_t*>(a.scores) + slot * a.p.max_pages
                           : reinterpret_cast<uint32_t*>(rest);
   // eight lanes per page, D / 8 columns each
   constexpr int CPL = D / 8;
@@ -504,7 +503,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_page_score(SelectArgs a) {
 #pragma unroll
   for (int w = 0; w < kSelThreads / 32; ++w) eps = fmaxf(eps, s_eps[w]);
   if (stored) {
-    if (tid == 0) a.bounds[list * a.splits + split] = eps;
+    if (tid == 0) a.bounds[slot * a.splits + split] = eps;
     return;
   }
   pick_list<T, D>(a, u, h, keys, error_bound(eps), s_q,
@@ -733,13 +732,13 @@ __global__ void __launch_bounds__(kGroupThreads, 2) k_group_score(SelectArgs a) 
   }
 }
 
-// grid (units, Hkv): the lists from stored scores (GROUP: those of k_group_score)
+// grid (units, heads) of a batch: the lists from stored scores (GROUP: those of k_group_score)
 template <typename T, int D, bool GROUP>
 __global__ void __launch_bounds__(kSelThreads) k_page_pick(SelectArgs a) {
   extern __shared__ __align__(16) unsigned char sm_sel[];
   __shared__ int sm_find[kSelThreads / 32 + 8];
   __shared__ double s_q[D];
-  const int unit = blockIdx.x, h = blockIdx.y;
+  const int unit = a.v0 + blockIdx.x, h = a.h0 + blockIdx.y;
   UnitInfo u;
   int* hist = reinterpret_cast<int*>(sm_sel);
   unsigned char* rest = sm_sel + kSelBins * 4;
@@ -756,9 +755,9 @@ __global__ void __launch_bounds__(kSelThreads) k_page_pick(SelectArgs a) {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the scores are complete
     if (!any) return;
   }
-  const size_t list = (size_t)unit * a.p.Hkv + h;
-  const uint32_t* keys = reinterpret_cast<const uint32_t*>(a.scores) + list * a.p.max_pages;
-  unsigned long long* keys64 = a.keys + list * a.p.max_pages;
+  const size_t list = (size_t)unit * a.p.Hkv + h, held = GROUP ? list : (size_t)(unit - a.u0) * a.nh + blockIdx.y;
+  const uint32_t* keys = reinterpret_cast<const uint32_t*>(a.scores) + held * a.p.max_pages;
+  unsigned long long* keys64 = a.keys + ((size_t)blockIdx.x * a.nh + blockIdx.y) * a.p.max_pages;
   if (!a.keys_global) {
     uint32_t* mine = reinterpret_cast<uint32_t*>(rest);
     for (int j = threadIdx.x; j < u.vis; j += kSelThreads) mine[j] = keys[j];
@@ -766,60 +765,89 @@ __global__ void __launch_bounds__(kSelThreads) k_page_pick(SelectArgs a) {
     keys64 = reinterpret_cast<unsigned long long*>(rest + (((size_t)a.p.max_pages * 4 + 15) & ~(size_t)15));
   }
   float eps = 0.f;
-  for (int s = 0; s < a.splits; ++s) eps = fmaxf(eps, a.bounds[list * a.splits + s]);
+  for (int s = 0; s < a.splits; ++s) eps = fmaxf(eps, a.bounds[held * a.splits + s]);
   __syncthreads();
   pick_list<T, D>(a, u, h, keys, error_bound(eps), s_q, keys64, hist, a.sel + list * a.p.n_select, a.cnt + list);
 }
 
 template <typename T, int D>
-cudaError_t launch_select_t(const SelectArgs& a, int* launches, cudaStream_t st) {
+cudaError_t launch_select_t(SelectArgs a, const SelectPlan& sp, int* launches, cudaStream_t st) {
   const size_t red = (size_t)(kSelThreads / (D / 8)) * (D + 1) * 8;
   const size_t keys = (((size_t)a.p.max_pages * 4 + 15) & ~(size_t)15) + (size_t)a.p.max_pages * 8;
   const bool stored = a.splits > 1 || a.keys_global;
   const size_t all = kSelBins * 4 + (a.keys_global || keys < red ? red : keys), score = kSelBins * 4 + (stored ? red : all - kSelBins * 4);
   cudaError_t e;
-  auto pick = [&](auto kern) -> cudaError_t {
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
-    if (err != cudaSuccess) return err;
-    ++*launches;
-    return launch_early(kern, dim3((unsigned)a.units, a.p.Hkv), kSelThreads, all, st, a);
-  };
   *launches = 0;
+  a.nh = sp.bh;
   if (a.group) {
     k_unit_mean<T, D><<<dim3((unsigned)a.units, a.p.Hkv), kGroupThreads, 0, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const unsigned groups = (unsigned)((a.units - 1) / kSelGroup + 1);
     if ((e = launch_early(k_group_score<T, D>, dim3(groups * a.splits, a.p.Hkv), kGroupThreads, 0, st, a)) != cudaSuccess) return e;
     *launches = 2;
-    return pick(k_page_pick<T, D, true>);
+    e = cudaFuncSetAttribute(k_page_pick<T, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
+  } else {
+    e = cudaFuncSetAttribute(k_page_score<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)score);
+    if (e == cudaSuccess && stored)
+      e = cudaFuncSetAttribute(k_page_pick<T, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
   }
-  e = cudaFuncSetAttribute(k_page_score<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)score);
   if (e != cudaSuccess) return e;
-  k_page_score<T, D><<<dim3((unsigned)a.units * a.splits, a.p.Hkv), kSelThreads, score, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  *launches = 1;
-  return stored ? pick(k_page_pick<T, D, false>) : cudaSuccess;
+  auto upto = [](int all, int at, int step) { return (unsigned)(all - at < step ? all - at : step); };
+  for (a.h0 = 0; a.h0 < a.p.Hkv; a.h0 += sp.bh)
+    for (a.u0 = 0; a.u0 < a.units; a.u0 += sp.bu) {
+      const unsigned nu = upto(a.units, a.u0, sp.bu), nh = upto(a.p.Hkv, a.h0, sp.bh);
+      if (!a.group) {
+        k_page_score<T, D><<<dim3(nu * a.splits, nh), kSelThreads, score, st>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        ++*launches;
+        if (!stored) continue;
+      }
+      for (a.v0 = a.u0; a.v0 < a.u0 + (int)nu; a.v0 += sp.bv) {
+        const dim3 grid(upto(a.u0 + (int)nu, a.v0, sp.bv), nh);
+        e = a.group ? launch_early(k_page_pick<T, D, true>, grid, kSelThreads, all, st, a)
+                    : launch_early(k_page_pick<T, D, false>, grid, kSelThreads, all, st, a);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+      }
+    }
+  return cudaSuccess;
 }
 
 template <typename T>
-cudaError_t launch_select_d(const SelectArgs& a, int d, int* launches, cudaStream_t st) {
-  return d == 64 ? launch_select_t<T, 64>(a, launches, st) : launch_select_t<T, 128>(a, launches, st);
+cudaError_t launch_select_d(const SelectArgs& a, const SelectPlan& sp, int d, int* launches, cudaStream_t st) {
+  return d == 64 ? launch_select_t<T, 64>(a, sp, launches, st) : launch_select_t<T, 128>(a, sp, launches, st);
 }
 
 }  // namespace
 
 // Splits of a unit's (or group's) pages: enough blocks for two per SM, at least 256 pages each.
+// Lists too long for shared memory keep their scores and 64-bit keys in the workspace, in batches of as
+// many lists as kSelWork holds of each, one at least (2,048 units of 8 heads over 16,384 pages: 0.54
+// instead of 3.3 GB, 15.6 instead of 15.0 ms).
 SelectPlan select_plan(int units, int Hkv, int max_pages, int B) {
-  SelectPlan p{1, max_pages > kSelSmemPages, false};
-  const long long blocks = (long long)units * Hkv;
+  SelectPlan p{1, max_pages > kSelSmemPages, false, units, units, Hkv};
+  long long blocks = (long long)units * Hkv;
   // groups of mostly one sequence, and scores that a workspace may hold (4 bytes per list and page)
-  if (units >= kSelGroup * (long long)B && blocks >= 64 && blocks * max_pages <= kSelScores) {
-    p.group = true;
+  p.group = units >= kSelGroup * (long long)B && blocks >= 64 && blocks * max_pages <= kSelWork / 4;
+  if (p.keys_global) {
+    auto fit = [&](int bytes, long long lists) -> int {     // of `lists`, at least one
+      const long long n = kSelWork / ((long long)bytes * max_pages);
+      return (int)(n < 1 ? 1 : (n < lists ? n : lists));
+    };
+    if (fit(8, blocks) < blocks) {
+      p.bh = fit(8, Hkv);
+      p.bv = fit(8, blocks) / p.bh;
+      if (!p.group) p.bu = fit(4, blocks) / p.bh;
+      p.bu = p.bu < units ? p.bu : units;
+    }
+  }
+  if (p.group) {
     const long long groups = ceil_div64(units, kSelGroup) * (long long)Hkv, most = ceil_div(max_pages, 256);
     const long long s = 296 / groups < most ? 296 / groups : most;
     p.splits = s < 1 ? 1 : (int)s;
     return p;
   }
+  blocks = (long long)p.bu * p.bh;
   if (blocks > 0 && blocks < 148) {
     long long s = 296 / blocks;
     const long long most = ceil_div(max_pages, 256);
@@ -829,9 +857,9 @@ SelectPlan select_plan(int units, int Hkv, int max_pages, int B) {
   return p;
 }
 
-cudaError_t launch_page_select(const SelectArgs& a, int d, int dtype, int* launches, cudaStream_t st) {
-  return dtype == SPARSEPR_FP16 ? launch_select_d<__half>(a, d, launches, st)
-                                : launch_select_d<__nv_bfloat16>(a, d, launches, st);
+cudaError_t launch_page_select(const SelectArgs& a, const SelectPlan& sp, int d, int dtype, int* launches, cudaStream_t st) {
+  return dtype == SPARSEPR_FP16 ? launch_select_d<__half>(a, sp, d, launches, st)
+                                : launch_select_d<__nv_bfloat16>(a, sp, d, launches, st);
 }
 
 }  // namespace spr

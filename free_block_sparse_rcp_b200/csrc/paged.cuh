@@ -310,9 +310,12 @@ struct SelectArgs {
   const void* km;
   int* sel;
   int* cnt;
-  float* scores;                  // [units][Hkv][max_pages] and
-  float* bounds;                  // [units][Hkv][splits], used with splits > 1 or `group`
-  unsigned long long* keys;       // [units][Hkv][max_pages], used when `keys_global`
+  // A batch of lists: units u0 .. u0 + bu - 1 (scores) or v0 .. (keys), heads h0 .. h0 + nh - 1
+  int u0, v0, h0, nh;
+  float* scores;                  // [unit - u0][h - h0][max_pages] (group: [units][Hkv][max_pages]) and
+  float* bounds;                  // [unit - u0][h - h0][splits] (group: [units][Hkv][splits]), used with
+                                  // splits > 1, `keys_global` or `group`
+  unsigned long long* keys;       // [unit - v0][h - h0][max_pages], used when `keys_global`
   double* qbar;                   // [units][Hkv][d] and
   int2* info;                     // [units] sequence and visible pages, used when `group`
   int n_sink, n_recent, units, splits;
@@ -322,9 +325,12 @@ struct SelectPlan {
   int splits;
   bool keys_global;
   bool group;       // four units' scores together
+  int bu, bv, bh;   // units and heads whose scores (bu x bh) and keys (bv x bh) are kept at once: all,
+                    // unless they would need more than kSelWork bytes
 };
+constexpr long long kSelWork = 1ll << 28;
 SelectPlan select_plan(int units, int Hkv, int max_pages, int B);
-cudaError_t launch_page_select(const SelectArgs& a, int d, int dtype, int* launches, cudaStream_t st);
+cudaError_t launch_page_select(const SelectArgs& a, const SelectPlan& sp, int d, int dtype, int* launches, cudaStream_t st);
 
 // rows kernel: items of at most 16 * mt query rows on mma.sync; tile kernel: 256-row items on
 // tcgen05; combine: the join of split items.

@@ -232,14 +232,16 @@ Layout layout_of(const sparsepr_cache_params& p) {
   L.plan_seq = take(items ? (p.B + 1ull) * 4 : 0);
   L.plan_item = take(items * 4);
   L.plan_pre = take(items * p.Hkv * 8);
-  // selection: scores of split lists, and 64-bit keys of lists too long for shared memory
+  // selection: scores of split lists, of units scored together and of lists too long for shared memory,
+  // and the latter's 64-bit keys (a batch of lists at a time)
   size_t scores = 0, bounds = 0, keys = 0, qbar = 0, info = 0;
   if (p.n_select > 0) {
     const size_t lists = (size_t)select_units(p) * p.Hkv;
     const SelectPlan sp = select_plan(select_units(p), p.Hkv, p.max_pages, p.B);
-    if (sp.splits > 1 || sp.keys_global || sp.group) scores = lists * p.max_pages * 4;
-    bounds = lists * sp.splits * 4;
-    if (sp.keys_global) keys = lists * p.max_pages * 8;
+    const size_t held = sp.group ? lists : (size_t)sp.bu * sp.bh;
+    if (sp.splits > 1 || sp.keys_global || sp.group) scores = held * p.max_pages * 4;
+    bounds = held * sp.splits * 4;
+    if (sp.keys_global) keys = (size_t)sp.bv * sp.bh * p.max_pages * 8;
     if (sp.group) {
       qbar = lists * p.d * 8;
       info = (size_t)select_units(p) * 8;
@@ -393,7 +395,7 @@ sparsepr_status sparsepr_page_select(const sparsepr_cache_params* p, const void*
   a.qbar = at<double>(workspace, L.qbar);
   a.info = at<int2>(workspace, L.info);
   int launches = 0;
-  const cudaError_t e = launch_page_select(a, p->d, p->dtype, &launches, (cudaStream_t)stream);
+  const cudaError_t e = launch_page_select(a, sp, p->d, p->dtype, &launches, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "launch_page_select");
   set_launch_count(launches);
   return SPARSEPR_OK;

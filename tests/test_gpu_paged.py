@@ -843,6 +843,39 @@ def test_select_many_pages(spr, gpu, Hkv, T):
     assert torch.all(cnt == 700)
 
 
+@pytest.mark.parametrize("B,n,Hkv,npg", [
+    (1, 240, 16, 9000),         # units scored together, their lists picked in two batches
+    (100, 5, 16, 9000),         # batches of units, scores and picks
+    (1, 2, 100, 400_000),       # batches of heads
+])
+def test_select_in_batches(spr, gpu, B, n, Hkv, npg):
+    """More lists of more pages than the workspace holds scores and keys for at once, many pages
+    with the same mean (ties by the hundred, decided in 64 bits)."""
+    page, d, T, K, sink, recent = 16, 64, B * n, 300, 2, 5
+    g = gen(98)
+    km = torch.randn(64, Hkv, d, generator=g).to(BF)
+    table = torch.randint(0, 64, (B, npg), generator=g).to(torch.int32)
+    p = spr.CacheParams.make(B, Hkv, Hkv, d, page=page, n_pages=64, max_pages=npg, T=T, max_chunk=n, q_block=1, n_select=K,
+                             n_sink=sink, n_recent=recent)
+    Q = torch.randn(T, Hkv, d, generator=g).to(BF)
+    kv = [npg * page - 700 * (b % 7) for b in range(B)]
+    ws = spr.paged_workspace(p, gpu)
+    sel, cnt = spr.alloc_selection(p, gpu)
+    sel.fill_(-9)
+    spr.sparsepr_page_select(p, Q.to(gpu), torch.arange(0, T + 1, n, dtype=torch.int32, device=gpu),
+                             torch.tensor(kv, dtype=torch.int32, device=gpu), table.to(gpu), km.to(gpu), sel, cnt, ws)
+    assert spr.sparsepr_paged_error(ws) == 0 and torch.all(cnt == K)
+    score = torch.einsum("thd,phd->thp", Q.double(), km.double())          # the 64 scores there are
+    sel = sel.cpu()
+    for t in range(T):
+        b, i = divmod(t, n)
+        vis = -(-(kv[b] - n + i + 1) // page)
+        s = score[t][:, table[b, :vis].long()]
+        s[:, :sink] = s[:, vis - recent:] = math.inf
+        want = torch.sort(s, dim=-1, descending=True, stable=True).indices[:, :K].sort(-1).values
+        assert torch.equal(sel[t].long(), want), t
+
+
 def test_bad_lists_are_errors(spr, gpu):
     for new, tiles in (([1, 1], False), ([40, 40], False), ([40, 40], True)):
         for what in ("order", "range", "count", "negative", "twice"):

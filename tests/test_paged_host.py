@@ -176,6 +176,21 @@ def test_workspace_holds_the_pieces(spr):
     assert spr.sparsepr_paged_workspace_bytes(_cache(spr, q_block=1, **chunk)) < 1 << 28
 
 
+@pytest.mark.parametrize("T,q_block,Hkv,max_pages", [
+    (32768, 1, 8, 8193), (32768, 1, 8, 16384), (32768, 64, 8, 16384), (4096, 1, 8, 16384), (32768, 1, 8, 1 << 20),
+    (300, 1, 4096, 20000), (1, 1, 4096, 1 << 20), (16384, 4, 2, 8192),
+])
+def test_workspace_of_long_lists_is_bounded(spr, T, q_block, Hkv, max_pages):
+    """Scores and 64-bit keys of lists beyond shared memory are kept for a batch of lists at a time: 256 MB
+    each at most beside what the call has without a selection, whatever the number of lists."""
+    kw = dict(B=1, T=T, max_chunk=T, Hq=Hkv, Hkv=Hkv, page=16, max_pages=max_pages, n_pages=100)
+    plain = spr.sparsepr_paged_workspace_bytes(_cache(spr, **kw))
+    sel = spr.sparsepr_paged_workspace_bytes(_cache(spr, n_select=64, q_block=q_block, **kw))
+    units = -(-T // q_block)
+    # 8 d + 16 bytes per list: mean queries, their sequences, error bounds
+    assert 0 < plain <= sel <= plain + (2 << 28) + 2 * units * Hkv * (8 * 64 + 16) + 4096
+
+
 @pytest.mark.parametrize("kw", [dict(), dict(n_select=4, q_block=40), dict(Hq=4096, Hkv=1, n_select=4, q_block=40)])
 def test_limits_beyond_the_rows_of_the_call(spr, kw):
     """A max_chunk or q_block that no sequence can reach counts as T: same plan, same workspace."""
