@@ -16,8 +16,8 @@
 // bits cost 8 integer instructions per element to widen the 16-bit means and took 40 us for 256
 // lists of up to 1,024 pages.
 //
-// Work: the means are read once per unit (1 / page of the keys' bytes), 4 d operations per page;
-// the queries once.  One block per (unit, head), or several that share its pages when there are
+// Work: the means are read once per unit, or once per four units scored together (1 / page of the
+// keys' bytes each time), 4 d operations per unit and page; the queries once.  One block per (unit, head), or several that share its pages when there are
 // few units; the selection then runs as a second kernel over the stored scores, which finds its unit
 // and mean query while the scores are made (5 units of a 475-token call over 36,000 keys, with their
 // attention: 34.5 us, 39.6 without).

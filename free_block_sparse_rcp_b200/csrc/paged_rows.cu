@@ -726,8 +726,8 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int page, int max_pages, int T, int
     p.S = items * Hkv < once ? once : (p.mt == 1 ? 4 : 2) * once;
     return p;
   }
-  // lists are equally long: one round of CTAs (256 lists of 64 pages of 64 keys take 126 us uncut
-  // and 145 us in four pieces)
+  // lists are equally long: one round of CTAs (256 lists of 64 pages of 64 keys with their selection
+  // take 126 us uncut, 96 of them here, and 145 us in four pieces)
   const long long most = ceil_div64((long long)max_pages * page, kPagedRowsBN) / p.min_split;
   long long S = items * Hkv > 0 ? once / (items * Hkv) : 1;
   S = S < most ? S : most;

@@ -27,9 +27,9 @@
 // ends.  The pieces of a cut entry are joined by k_tiles_join.
 //
 // Bounds.  d = 128: a chunk of both tiles takes 1.65 us, and long calls run into the power limit besides:
-// 4,680 tokens x 40 heads over 32,760 keys take 2.65 ms, 1,130 TFLOP/s, the last 1,024-token frame of
-// 4 x 16 heads over 16,384 keys 545 us, 1,010 TFLOP/s (457 us in a single launch, before the clock
-// falls).  d = 64: half the products, as many exponentials: a chunk of both tiles takes 1.45 us, and
+// 4,680 tokens x 40 heads over 32,760 keys take 2.65 to 2.71 ms from one GPU to another, 1,130 to 1,105
+// TFLOP/s, the last 1,024-token frame of 4 x 16 heads over 16,384 keys 545 to 562 us, 1,010 to 980
+// TFLOP/s (457 us in a single launch, before the clock falls).  d = 64: half the products, as many exponentials: a chunk of both tiles takes 1.45 us, and
 // the unit that computes exponentials 1.18 us of it; six ragged chunks (87 GFLOP) take 173 us.
 // Measured without gain: keys in double-buffered halves (N = 64 products take as long as N = 128: 2.0
 // us per chunk), a quarter or half of the exponentials as polynomials in the FMA units, P handed

@@ -5,7 +5,7 @@
 // the gradient is the same with -t.  Both kernels move every row once and are bound by
 // memory, so a thread keeps the sines and cosines of its pairs in registers, where they serve
 // the heads of the token.
-// Measured: 32,760 tokens x 80 heads of d 128, bf16 (1.34 GB) 210 us, 6.4 TB/s, a copy's rate; 2 x
+// Measured: 32,760 tokens x 80 heads of d 128, bf16 (1.34 GB) 212 us, 6.3 TB/s, a copy's rate; 2 x
 // 5,003 tokens x 40 heads, fp32, half of d turned (410 MB) 79 us, 5.2 TB/s; 64 single tokens
 // 3.8 us, the latency of one launch with a 64-bit product and a sine.
 // The turn count pos f is formed and reduced to [-1/2, 1/2] in 64 bits: in 32 bits the
@@ -298,7 +298,7 @@ cudaError_t launch_rope_m(const RopeArgs& a, cudaStream_t st) {
 // r mod RG, the groups are added in order), so the mean depends on the page's contents alone.
 // Both together in one block per page had to hold a page's angles in shared memory and its blocks
 // waited for one another's latencies: 38 us for 4 x 1,024 tokens of 16 heads (d 128) on pages of
-// 128, against 18.7 us for the two and the 10 us that the 67 MB need; what is left is the latency of
+// 128, against 18.9 us for the two and the 10 us that the 67 MB need; what is left is the latency of
 // two short kernels (angle, load, store; then table, rows, mean).  One token of each of 64
 // sequences takes 6.8 us.
 

@@ -337,8 +337,9 @@ SPARSEPR_API sparsepr_status sparsepr_workspace_clear_error(const sparsepr_param
  * with (a, b) = (i, i + rot_dim/2) (layout 0, halves) or (2i, 2i + 1) (layout 1,
  * interleaved); elements rot_dim .. d-1 are copied.  The pairs are divided into n_axes
  * consecutive sections of axis_dim[a]/2 pairs (time, height, width of a video latent; one
- * axis for text-like sequences).  Angles are reduced in 64 bits, so that positions up to
- * 2^31 keep full accuracy.                                                             */
+ * axis for text-like sequences).  Angles are formed and reduced in 64 bits and are off by a
+ * few 2^-53 |pos| rad: below fp32's half step of 2^-24 up to positions of 2^27, 10^-6 at 2^31
+ * (16-bit rows round more coarsely than that at every position).                       */
 typedef struct {
   int B, H, N, d;          /* batch, heads, tokens (0 is allowed), head dim (2..512)                */
   int H2;                  /* heads of the second tensor of the call (0: none)                      */
@@ -457,7 +458,9 @@ SPARSEPR_API sparsepr_status sparsepr_cache_append(const sparsepr_cache_params* 
  *   sel       int32 [units, Hkv, n_select]  page indices within the sequence, ascending, -1 behind
  *   sel_count int32 [units, Hkv]            entries of each list
  * Rows of units that do not exist are left as they were.  A page id out of [0, n_pages) is
- * device error 1 and counts as the lowest score.                                        */
+ * device error 1 and counts as the lowest score.  With more than 8,192 pages per sequence the
+ * lists are made in batches, so that the workspace holds at most 256 MB of scores and 256 MB
+ * of keys (or 12 bytes per page of one list, if that is more).                          */
 SPARSEPR_API int sparsepr_select_units(const sparsepr_cache_params* p);
 SPARSEPR_API sparsepr_status sparsepr_page_select(const sparsepr_cache_params* p, const void* Q, const int* q_start,
                                                   const int* kv_len, const int* page_table, const void* k_mean,
