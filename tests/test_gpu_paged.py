@@ -367,6 +367,14 @@ def test_attention_many_small_weights_fp16(spr, gpu, new, kv, tiles):
     s.check(*s.attend())
 
 
+@pytest.mark.parametrize("new,kv,tiles", [([1, 3], [900, 70], False), ([60], [300], False), ([60], [300], True)])
+@pytest.mark.parametrize("scale", [0.03125, 0.375])
+def test_attention_scale_of_the_caller(spr, gpu, new, kv, tiles, scale):
+    s = Scene(spr, gpu, new, kv, Hq=4, Hkv=2, d=64, page=32, dt=BF, seed=101, tiles=tiles)
+    s.p.scale = s.scale = scale
+    s.check(*s.attend())
+
+
 @pytest.mark.parametrize("tiles", [False, True])
 def test_a_list_longer_than_the_cache_is_an_error(spr, gpu, tiles):
     """Every page once and the last one again, behind the chunks that the visible keys need."""
